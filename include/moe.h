@@ -38,7 +38,8 @@
  *   - Matrices of weights are stored [out][in] (the reduction dimension is
  *     contiguous).  bf16 is stored as its 16-bit pattern; e4m3 is OCP E4M3FN
  *     (largest finite 448) in one byte.
- *   - Inputs must be finite; NaN and infinity are not checked.
+ *   - Inputs must be finite; NaN and infinity are not checked (the gate and MX4
+ *     calls say what they make of them).
  *   - Calls on different streams that share a buffer race, workspaces
  *     included (a workspace holds intermediate results and the expert
  *     kernel's tile-queue counters); the library holds no global mutable
@@ -344,6 +345,132 @@ int moe_backward_timed(const moe_shape *shape, const void *u, const void *gate_w
 
 /* Workspace bytes for moe_backward (0 when rejected). */
 size_t moe_backward_workspace_bytes(const moe_shape *shape);
+
+/* ------------------------------------------------------------------------ */
+/* gate: routing from logits                                                */
+
+enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
+
+/* moe_gate_rule.flags */
+#define MOE_GATE_RENORM 1u      /* weights are divided by their sum */
+#define MOE_GATE_GROUP_MAX 2u   /* a group scores its largest choice value, else the sum of its two largest */
+
+/*
+ * How a gate scores, chooses and weighs.  Limits (MOE_ERR_UNSUPPORTED
+ * otherwise): n_experts <= 1024, n_experts % n_groups == 0,
+ * 1 <= topk_groups <= n_groups <= 64, 1 <= topk <= 32,
+ * topk <= topk_groups * n_experts / n_groups, T * topk < 2^31.
+ */
+typedef struct moe_gate_rule {
+    int64_t T;              /* tokens (T >= 0; T == 0 is a no-op) */
+    int32_t n_experts;
+    int32_t n_groups;       /* group g = experts [g * n_experts / n_groups, ...); 1: no groups */
+    int32_t topk_groups;    /* groups a token may use */
+    int32_t topk;           /* K: experts per token */
+    int32_t score;          /* MOE_SCORE_SIGMOID | MOE_SCORE_SOFTMAX */
+    int32_t logits_dtype;   /* logits and dlogits: MOE_F32 | MOE_BF16 */
+    float routed_scale;     /* factor on every weight */
+    uint32_t flags;         /* MOE_GATE_RENORM | MOE_GATE_GROUP_MAX, or 0 */
+} moe_gate_rule;
+
+/*
+ * moe_gate -- scores, choice and weights from the logits z of any gate product
+ * (moe_route has its own gate product and sigmoid scores only):
+ *   s_i = 1 / (1 + exp(-z_i)), or
+ *   s_i = exp(z_i - max z) * (1 / sum_k exp(z_k - max z)), the sum rounded once to fp32;
+ *   a logit of -infinity or NaN is an expert out of use: s_i = 0;
+ *   choice value c_i = s_i + bias_i (one fp32 add), -infinity for an expert out
+ *     of use or where the sum is NaN;
+ *   a group's score is the sum of its two largest c (its only one where one is
+ *     above -infinity), or its largest; the topk_groups best groups are kept,
+ *     the c of the others become -infinity;
+ *   topk_idx[t] = the topk largest c in decreasing order; every tie goes to the
+ *     lower index;
+ *   topk_w[t][j] = routed_scale * s_j, with MOE_GATE_RENORM routed_scale *
+ *     (s_j / (s_0 + ... + s_{K-1})), the sum from left to right; 0 where
+ *     c_j = -infinity (fewer experts in use than slots: such slots hold the
+ *     lowest indices left, so that a token's experts stay distinct and
+ *     moe_permute takes them) and where the sum is 0.
+ * logits [T] rows of n_experts values, ld elements apart (ld >= n_experts);
+ * bias [n_experts] fp32 or NULL; scores_out [T][n_experts] fp32 or NULL;
+ * topk_idx [T][K] int32; topk_w [T][K] fp32.  All arithmetic is fp32 (the
+ * softmax sum fp64).  No workspace.
+ */
+int moe_gate(const moe_gate_rule *rule, const void *logits, int64_t ld, const float *bias, float *scores_out,
+             int32_t *topk_idx, float *topk_w, void *stream);
+
+/*
+ * moe_gate_backward -- dL/dz for the choice that moe_gate made (the choice is
+ * piecewise constant: it and the bias take no gradient).  With g = dtopk_w,
+ * S = routed_scale, D = sum of the chosen s, over the slots whose weight is not 0:
+ *   ds_j = S g_j, with MOE_GATE_RENORM S (g_j - sum_k g_k s_k / D) / D,
+ *   plus dscores_i at every expert when dscores is given (a loss on scores_out);
+ *   sigmoid: dz_i = ds_i s_i (1 - s_i);  softmax: dz_i = s_i (ds_i - sum_k ds_k s_k).
+ * An expert out of use gets 0.  s is recomputed from the logits.
+ * logits, ld, topk_idx, topk_w as given to and by moe_gate (indices distinct
+ * within a token); dtopk_w [T][K] fp32; dscores [T][n_experts] fp32 or NULL;
+ * dlogits [T] rows of n_experts values in logits_dtype, dld elements apart,
+ * every one of which is written.  Sums run in fp32 in a fixed order.
+ */
+int moe_gate_backward(const moe_gate_rule *rule, const void *logits, int64_t ld, const int32_t *topk_idx,
+                      const float *topk_w, const float *dtopk_w, const float *dscores, void *dlogits, int64_t dld,
+                      void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* MX4: microscaled 4-bit floating point                                    */
+
+/*
+ * An MX4 matrix (OCP Microscaling Formats v1.0, element type E2M1, scale type
+ * E8M0): blocks of 32 values along a row share a scale 2^(s - 127) held in one
+ * byte s; a value is a 4-bit code (sign, then 0, 0.5, 1, 1.5, 2, 3, 4, 6) times
+ * its block's scale.  A row of `cols` values takes R = ceil(cols / 128) runs:
+ * 64 R code bytes (value 2i in the low half of byte i) and 4 R scale bytes;
+ * what lies past the last value is 0 (codes 0; scale 127 in blocks of zeros).
+ * With cols % 128 == 0 the rows are thus cols / 2 and cols / 32 dense bytes.
+ * Code arrays must be 16-byte aligned and scale arrays 4-byte aligned.
+ */
+
+/*
+ * moe_quantize_mx4 -- x [rows] rows of cols values (x_dtype MOE_F32 or
+ * MOE_BF16), ld elements apart, to codes q [rows][64 R] and scales s [rows][4 R]:
+ * s = max(exponent field of the block's largest magnitude - 2, 0), 127 for a
+ * block of zeros; code = nearest to x / 2^(s - 127), ties to the even code,
+ * magnitudes above 6 to 6 (the largest scaled magnitude lies in [4, 8)).
+ * A block that holds an infinity or NaN gets s = 255 (NaN) and codes 0.
+ */
+int moe_quantize_mx4(int64_t rows, int32_t cols, int32_t x_dtype, const void *x, int64_t ld, uint8_t *q, uint8_t *s,
+                     void *stream);
+
+/*
+ * moe_dequantize_mx4 -- the values of codes q and scales s as y_dtype (MOE_F32 or
+ * MOE_BF16), rows ld elements apart.  Exact in both types (s = 255 gives NaN).
+ * quantise + dequantise is the rounding of training with MX4 weights: the bf16
+ * values go through moe_forward and moe_backward, whose weight gradients are
+ * then those of the unrounded weights by the straight-through rule.
+ */
+int moe_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t *q, const uint8_t *s, int32_t y_dtype, void *y,
+                       int64_t ld, void *stream);
+
+/*
+ * moe_grouped_ffn_mx4 -- moe_grouped_ffn on MX4 weights and activations:
+ *   a = W_gate[e] x_r,  b = W_up[e] x_r,  h = Q(a / (1 + exp(-a)) * b),  y[r] = W_down[e] h
+ * for the rows r in [offsets[e], offsets[e+1]) of expert e, x_r = x[gather[r]]
+ * (gather NULL: x[r]); Q is moe_quantize_mx4's rounding of the fp32 values;
+ * products of codes and scales are summed in fp32; y [max_rows][d] is bf16.
+ * n_exp <= 1024 experts; offsets [n_exp+1] int32 on the device, offsets[0] = 0,
+ * non-decreasing, offsets[n_exp] <= max_rows.  d and inter are any positive
+ * sizes (rows padded to whole runs as above).
+ * x codes, x_scales [*]; w = {W_gate, W_up, W_down} codes [n_exp][inter] rows of d,
+ * [n_exp][inter] of d, [n_exp][d] rows of inter; w_scales their scales.
+ * (The arrays of 3 pointers are host memory, their elements device pointers.)
+ * ws: moe_ffn_mx4_workspace_bytes(max_rows, inter).
+ */
+int moe_grouped_ffn_mx4(int32_t n_exp, const int32_t *offsets, int64_t max_rows, const int32_t *gather, int32_t d,
+                        int32_t inter, const uint8_t *x, const uint8_t *x_scales, const uint8_t *const *w,
+                        const uint8_t *const *w_scales, void *y, void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes for moe_grouped_ffn_mx4: 68 bytes a row and run of 128 of inter, and less than 1 KB. */
+size_t moe_ffn_mx4_workspace_bytes(int64_t max_rows, int32_t inter);
 
 /* ------------------------------------------------------------------------ */
 /* helpers                                                                  */

@@ -26,6 +26,8 @@ MOE_F32, MOE_BF16, MOE_E4M3 = 0, 1, 2
 MOE_ADD_RESIDUAL = 1
 MOE_SAVE_SWIGLU_INPUTS = 2   # moe_forward keeps the SwiGLU inputs for moe_backward
 MOE_WS_ROUTE, MOE_WS_PERMUTE, MOE_WS_FORWARD = 0, 1, 2
+MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
+MOE_GATE_RENORM, MOE_GATE_GROUP_MAX = 1, 2   # MoeGateRule.flags
 MOE_STATIC_WS_BYTES = 64 << 20   # the library's own forward workspace per GPU (moe_forward_static)
 
 EXPORTED = ("moe_route", "moe_permute", "moe_grouped_ffn", "moe_combine", "moe_forward", "moe_forward_timed",
@@ -33,8 +35,9 @@ EXPORTED = ("moe_route", "moe_permute", "moe_grouped_ffn", "moe_combine", "moe_f
             "moe_workspace_bytes",
             "moe_ffn_workspace_bytes", "moe_bias_update", "moe_seq_balance", "moe_seq_balance_workspace_bytes",
             "moe_transpose_expert_weights", "moe_backward", "moe_backward_timed", "moe_backward_workspace_bytes",
-            "moe_quantize_1x128", "moe_quantize_weights_128x128", "moe_quantize_128x1", "moe_last_error",
-            "moe_version")
+            "moe_quantize_1x128", "moe_quantize_weights_128x128", "moe_quantize_128x1", "moe_gate",
+            "moe_gate_backward", "moe_quantize_mx4", "moe_dequantize_mx4", "moe_grouped_ffn_mx4",
+            "moe_ffn_mx4_workspace_bytes", "moe_last_error", "moe_version")
 
 
 class MoeError(RuntimeError):
@@ -63,6 +66,27 @@ def make_shape(T, d, n_routed, n_shared, n_groups, topk_groups, topk, inter, dty
                     routed_scale, flags)
 
 
+class MoeGateRule(ctypes.Structure):
+    """moe_gate_rule of include/moe.h."""
+    _fields_ = [
+        ("T", ctypes.c_int64), ("n_experts", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32), ("topk", ctypes.c_int32), ("score", ctypes.c_int32),
+        ("logits_dtype", ctypes.c_int32), ("routed_scale", ctypes.c_float), ("flags", ctypes.c_uint32),
+    ]
+
+
+def make_gate_rule(T, n_experts, topk, score="sigmoid", n_groups=1, topk_groups=1, group_score="top2",
+                   renormalize=True, routed_scale=1.0, logits="fp32") -> MoeGateRule:
+    """score: "sigmoid" or "softmax"; group_score: "top2" (sum of a group's two largest choice values) or "max";
+    logits: "fp32" or "bf16"."""
+    if score not in ("sigmoid", "softmax") or group_score not in ("top2", "max") or logits not in ("fp32", "bf16"):
+        raise ValueError("score %r, group_score %r, logits %r" % (score, group_score, logits))
+    flags = (MOE_GATE_RENORM if renormalize else 0) | (MOE_GATE_GROUP_MAX if group_score == "max" else 0)
+    return MoeGateRule(T, n_experts, n_groups, topk_groups, topk,
+                       MOE_SCORE_SIGMOID if score == "sigmoid" else MOE_SCORE_SOFTMAX,
+                       MOE_F32 if logits == "fp32" else MOE_BF16, routed_scale, flags)
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -76,7 +100,7 @@ def lib():
                 raise MoeError(MOE_ERR_HIP, "libmoe.so is not built (run __graft_entry__.build())")
             L = ctypes.CDLL(LIB_PATH)
             P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
-            S = ctypes.POINTER(MoeShape)
+            S, R = ctypes.POINTER(MoeShape), ctypes.POINTER(MoeGateRule)
             sig = {
                 "moe_route": [S, P, P, P, P, P, P, P, P, sz, P],
                 "moe_permute": [S, P, P, P, P, P, P, P, P, P, sz, P],
@@ -93,6 +117,11 @@ def lib():
                 "moe_quantize_1x128": [i64, i32, i32, P, P, P, P],
                 "moe_quantize_weights_128x128": [i64, i32, i32, i32, P, P, P, P],
                 "moe_quantize_128x1": [i32, P, i64, i32, i32, P, P, P, P, P, P, P],
+                "moe_gate": [R, P, i64, P, P, P, P, P],
+                "moe_gate_backward": [R, P, i64, P, P, P, P, P, i64, P],
+                "moe_quantize_mx4": [i64, i32, i32, P, i64, P, P, P],
+                "moe_dequantize_mx4": [i64, i32, P, P, i32, P, i64, P],
+                "moe_grouped_ffn_mx4": [i32, P, i64, P, i32, i32, P, P, P, P, P, P, sz, P],
             }
             for name, args in sig.items():
                 f = getattr(L, name)
@@ -106,6 +135,8 @@ def lib():
             L.moe_seq_balance_workspace_bytes.restype = sz
             L.moe_backward_workspace_bytes.argtypes = [S]
             L.moe_backward_workspace_bytes.restype = sz
+            L.moe_ffn_mx4_workspace_bytes.argtypes = [i64, i32]
+            L.moe_ffn_mx4_workspace_bytes.restype = sz
             L.moe_last_error.argtypes = []
             L.moe_last_error.restype = ctypes.c_char_p
             L.moe_version.argtypes = []
@@ -318,3 +349,33 @@ def moe_quantize_128x1(n_seg, offsets, max_rows, cols, x_dtype, x, x_s, gather, 
 def moe_quantize_weights_128x128(nmat, rows, cols, w_dtype, w, q, s, stream=None):
     return _check(lib().moe_quantize_weights_128x128(nmat, rows, cols, w_dtype, _ptr(w), _ptr(q), _ptr(s),
                                                      _stream(stream)))
+
+
+def moe_gate(rule, logits, ld, bias, scores_out, topk_idx, topk_w, stream=None):
+    return _check(lib().moe_gate(ctypes.byref(rule), _ptr(logits), ld, _ptr(bias), _ptr(scores_out), _ptr(topk_idx),
+                                 _ptr(topk_w), _stream(stream)))
+
+
+def moe_gate_backward(rule, logits, ld, topk_idx, topk_w, dtopk_w, dscores, dlogits, dld, stream=None):
+    return _check(lib().moe_gate_backward(ctypes.byref(rule), _ptr(logits), ld, _ptr(topk_idx), _ptr(topk_w),
+                                          _ptr(dtopk_w), _ptr(dscores), _ptr(dlogits), dld, _stream(stream)))
+
+
+def moe_quantize_mx4(rows, cols, x_dtype, x, ld, q, s, stream=None):
+    return _check(lib().moe_quantize_mx4(rows, cols, x_dtype, _ptr(x), ld, _ptr(q), _ptr(s), _stream(stream)))
+
+
+def moe_dequantize_mx4(rows, cols, q, s, y_dtype, y, ld, stream=None):
+    return _check(lib().moe_dequantize_mx4(rows, cols, _ptr(q), _ptr(s), y_dtype, _ptr(y), ld, _stream(stream)))
+
+
+def moe_ffn_mx4_workspace_bytes(max_rows: int, inter: int) -> int:
+    return lib().moe_ffn_mx4_workspace_bytes(max_rows, inter)
+
+
+def moe_grouped_ffn_mx4(n_exp, offsets, max_rows, gather, d, inter, x, x_scales, w, w_scales, y, ws, stream=None):
+    """w, w_scales: codes and scales of (W_gate, W_up, W_down)."""
+    wa, sa = _ptr_array(w), _ptr_array(w_scales)
+    return _check(lib().moe_grouped_ffn_mx4(n_exp, _ptr(offsets), max_rows, _ptr(gather), d, inter, _ptr(x),
+                                            _ptr(x_scales), wa[0] if wa else None, sa[0] if sa else None, _ptr(y),
+                                            _ptr(ws), _nbytes(ws), _stream(stream)))

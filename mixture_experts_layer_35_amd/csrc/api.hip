@@ -1091,3 +1091,186 @@ int moe_quantize_128x1(int32_t n_seg, const int32_t *offsets, int64_t max_rows, 
 }
 
 }  // extern "C"
+
+// ---- gate on logits, MX4 ----------------------------------------------------------
+
+namespace {
+
+int check_gate(const moe_gate_rule *r, const char *fn) {
+    if (!r) return fail(MOE_ERR_INVALID_ARG, "%s: rule must not be NULL", fn);
+    if (r->T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: T = %lld is negative", fn, (long long)r->T);
+    if (r->n_experts <= 0 || r->n_groups <= 0 || r->topk_groups <= 0 || r->topk <= 0)
+        return fail(MOE_ERR_INVALID_ARG, "%s: sizes must be positive", fn);
+    if (r->score != MOE_SCORE_SIGMOID && r->score != MOE_SCORE_SOFTMAX)
+        return fail(MOE_ERR_INVALID_ARG, "%s: unknown score %d", fn, r->score);
+    if (r->flags & ~(MOE_GATE_RENORM | MOE_GATE_GROUP_MAX))
+        return fail(MOE_ERR_INVALID_ARG, "%s: unknown flags 0x%x", fn, r->flags);
+    if (r->logits_dtype != MOE_F32 && r->logits_dtype != MOE_BF16)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: logits_dtype %d", fn, r->logits_dtype);
+    if (r->n_experts > kMaxExperts)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: n_experts = %d exceeds %d", fn, r->n_experts, kMaxExperts);
+    if (r->n_experts % r->n_groups)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: n_experts = %d is not a multiple of n_groups = %d", fn, r->n_experts,
+                    r->n_groups);
+    if (r->n_groups > 64 || r->topk_groups > r->n_groups)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: need topk_groups <= n_groups <= 64 (got %d, %d)", fn, r->topk_groups,
+                    r->n_groups);
+    if (r->topk > 32 || (int64_t)r->topk > (int64_t)r->topk_groups * (r->n_experts / r->n_groups))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: topk = %d must be <= 32 and <= topk_groups * n_experts / n_groups", fn,
+                    r->topk);
+    if (r->T >= (1ll << 31) / r->topk) return fail(MOE_ERR_UNSUPPORTED, "%s: T * topk must be below 2^31", fn);
+    return MOE_OK;
+}
+
+GateProblem gate_problem(const moe_gate_rule *r, const void *logits, int64_t ld) {
+    return GateProblem{r->T, r->n_experts, r->n_groups, r->topk_groups, r->topk, r->score == MOE_SCORE_SOFTMAX,
+                       (r->flags & MOE_GATE_RENORM) != 0, (r->flags & MOE_GATE_GROUP_MAX) != 0, r->routed_scale,
+                       dt_of(r->logits_dtype), logits, ld};
+}
+
+// A pointer's elements must lie at multiples of their size.
+#define ALIGNED(ptr, bytes)                                                                                        \
+    do {                                                                                                           \
+        if ((uintptr_t)(ptr) % (bytes))                                                                            \
+            return fail(MOE_ERR_INVALID_ARG, "%s: %s must be %d-byte aligned", fn, #ptr, (int)(bytes));           \
+    } while (0)
+
+int check_mx4_matrix(int64_t rows, int32_t cols, int32_t dtype, int64_t ld, const char *fn) {
+    if (rows < 0 || cols <= 0) return fail(MOE_ERR_INVALID_ARG, "%s: bad size", fn);
+    if (ld < cols) return fail(MOE_ERR_INVALID_ARG, "%s: ld = %lld is below cols = %d", fn, (long long)ld, cols);
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
+    return MOE_OK;
+}
+
+size_t mx4_h_codes(int64_t max_rows, int32_t inter) { return align256((size_t)max_rows * mx4_runs(inter) * 64); }
+
+}  // namespace
+
+extern "C" {
+
+int moe_gate(const moe_gate_rule *rule, const void *logits, int64_t ld, const float *bias, float *scores_out,
+             int32_t *topk_idx, float *topk_w, void *stream) {
+    const char *fn = "moe_gate";
+    int rc = check_gate(rule, fn);
+    if (rc != MOE_OK) return rc;
+    if (ld < rule->n_experts) return fail(MOE_ERR_INVALID_ARG, "%s: ld = %lld is below n_experts", fn, (long long)ld);
+    if (rule->T == 0) return MOE_OK;
+    NEED(logits);
+    NEED(topk_idx);
+    NEED(topk_w);
+    ALIGNED(logits, esize(rule->logits_dtype));
+    HIPCHK(launch_gate(gate_problem(rule, logits, ld), bias, scores_out, topk_idx, topk_w, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+int moe_gate_backward(const moe_gate_rule *rule, const void *logits, int64_t ld, const int32_t *topk_idx,
+                      const float *topk_w, const float *dtopk_w, const float *dscores, void *dlogits, int64_t dld,
+                      void *stream) {
+    const char *fn = "moe_gate_backward";
+    int rc = check_gate(rule, fn);
+    if (rc != MOE_OK) return rc;
+    if (ld < rule->n_experts || dld < rule->n_experts)
+        return fail(MOE_ERR_INVALID_ARG, "%s: ld = %lld or dld = %lld is below n_experts", fn, (long long)ld,
+                    (long long)dld);
+    if (rule->T == 0) return MOE_OK;
+    NEED(logits);
+    NEED(topk_idx);
+    NEED(topk_w);
+    NEED(dtopk_w);
+    NEED(dlogits);
+    ALIGNED(logits, esize(rule->logits_dtype));
+    ALIGNED(dlogits, esize(rule->logits_dtype));
+    HIPCHK(launch_gate_backward(gate_problem(rule, logits, ld), topk_idx, topk_w, dtopk_w, dscores, dlogits, dld,
+                                (hipStream_t)stream));
+    return MOE_OK;
+}
+
+int moe_quantize_mx4(int64_t rows, int32_t cols, int32_t x_dtype, const void *x, int64_t ld, uint8_t *q, uint8_t *s,
+                     void *stream) {
+    const char *fn = "moe_quantize_mx4";
+    int rc = check_mx4_matrix(rows, cols, x_dtype, ld, fn);
+    if (rc != MOE_OK) return rc;
+    if (rows == 0) return MOE_OK;
+    NEED(x);
+    NEED(q);
+    NEED(s);
+    ALIGNED(x, esize(x_dtype));
+    ALIGNED(q, 16);
+    ALIGNED(s, 4);
+    HIPCHK(launch_mx4_quantize(dt_of(x_dtype), x, ld, rows, cols, q, s, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+int moe_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t *q, const uint8_t *s, int32_t y_dtype, void *y,
+                       int64_t ld, void *stream) {
+    const char *fn = "moe_dequantize_mx4";
+    int rc = check_mx4_matrix(rows, cols, y_dtype, ld, fn);
+    if (rc != MOE_OK) return rc;
+    if (rows == 0) return MOE_OK;
+    NEED(q);
+    NEED(s);
+    NEED(y);
+    ALIGNED(y, esize(y_dtype));
+    ALIGNED(q, 16);
+    ALIGNED(s, 4);
+    HIPCHK(launch_mx4_dequantize(dt_of(y_dtype), q, s, rows, cols, y, ld, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+size_t moe_ffn_mx4_workspace_bytes(int64_t max_rows, int32_t inter) {
+    if (max_rows < 0 || max_rows >= (1ll << 31) || inter <= 0) {
+        fail(MOE_ERR_INVALID_ARG, "moe_ffn_mx4_workspace_bytes: bad size");
+        return 0;
+    }
+    return mx4_h_codes(max_rows, inter) + align256((size_t)max_rows * mx4_runs(inter) * 4);
+}
+
+int moe_grouped_ffn_mx4(int32_t n_exp, const int32_t *offsets, int64_t max_rows, const int32_t *gather, int32_t d,
+                        int32_t inter, const uint8_t *x, const uint8_t *x_scales, const uint8_t *const *w,
+                        const uint8_t *const *w_scales, void *y, void *ws, size_t ws_bytes, void *stream) {
+    const char *fn = "moe_grouped_ffn_mx4";
+    if (n_exp <= 0 || d <= 0 || inter <= 0 || max_rows < 0)
+        return fail(MOE_ERR_INVALID_ARG, "%s: sizes must be positive (max_rows >= 0)", fn);
+    if (n_exp > kMaxExperts) return fail(MOE_ERR_UNSUPPORTED, "%s: n_exp = %d exceeds %d", fn, n_exp, kMaxExperts);
+    // tiles are counted in 32 bits; a weight row's codes and a tile's rows are addressed in 32 bits
+    const int64_t most = mx4_runs(d) * 128 > mx4_runs(inter) * 128 ? mx4_runs(d) * 128 : mx4_runs(inter) * 128;
+    if (max_rows >= (1ll << 31) || most > (1 << 20) || (max_rows / 16 + n_exp) * (most / 32) >= (1ll << 31))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: max_rows = %lld, d = %d, inter = %d are too large for one call", fn,
+                    (long long)max_rows, d, inter);
+    if (max_rows == 0) return MOE_OK;
+    NEED(offsets);
+    NEED(x);
+    NEED(x_scales);
+    NEED(w);
+    NEED(w_scales);
+    NEED(y);
+    ALIGNED(x, 16);
+    ALIGNED(x_scales, 4);
+    ALIGNED(y, 2);
+    Mx4Ffn a{};
+    for (int i = 0; i < 3; ++i) {
+        NEED(w[i]);
+        NEED(w_scales[i]);
+        ALIGNED(w[i], 16);
+        ALIGNED(w_scales[i], 4);
+        a.w[i] = w[i];
+        a.ws[i] = w_scales[i];
+    }
+    int rc = ws_check(ws, ws_bytes, moe_ffn_mx4_workspace_bytes(max_rows, inter), fn);
+    if (rc != MOE_OK) return rc;
+    a.n_exp = n_exp;
+    a.offsets = offsets;
+    a.max_rows = max_rows;
+    a.gather = gather;
+    a.d = d;
+    a.inter = inter;
+    a.x = x;
+    a.xs = x_scales;
+    a.h = (uint8_t *)ws;
+    a.hs = a.h + mx4_h_codes(max_rows, inter);
+    a.y = (uint16_t *)y;
+    HIPCHK(launch_mx4_ffn(a, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+}  // extern "C"

@@ -28,6 +28,40 @@ hipError_t launch_router_splitk(const void *u, const void *gate_w, float *part, 
 hipError_t launch_router_select(const float *scores, const float *bias, int64_t T, int Nr, int G, int Mg, int K,
                                 float routed_scale, int32_t *topk_idx, float *topk_w, hipStream_t s);
 
+// ---- gate on logits ----------------------------------------------------------
+struct GateProblem {
+    int64_t T;
+    int E, G, M, K;         // experts, groups, groups kept, slots
+    bool softmax, renorm, group_max;
+    float scale;
+    int dt;                 // of logits and dlogits: DT_F32 | DT_BF16
+    const void *logits;     // [T] rows, ld elements apart
+    int64_t ld;
+};
+hipError_t launch_gate(const GateProblem &p, const float *bias, float *scores, int32_t *idx, float *w, hipStream_t s);
+// dlogits from the forward's idx and w, dw = dL/dw and (or null) ds = dL/dscores.
+hipError_t launch_gate_backward(const GateProblem &p, const int32_t *idx, const float *w, const float *dw,
+                                const float *ds, void *dlogits, int64_t dld, hipStream_t s);
+
+// ---- MX4 ---------------------------------------------------------------------
+inline int64_t mx4_runs(int64_t cols) { return (cols + 127) / 128; }
+hipError_t launch_mx4_quantize(int dt, const void *x, int64_t ld, int64_t rows, int cols, uint8_t *q, uint8_t *sc,
+                               hipStream_t s);
+hipError_t launch_mx4_dequantize(int dt, const uint8_t *q, const uint8_t *sc, int64_t rows, int cols, void *y,
+                                 int64_t ld, hipStream_t s);
+struct Mx4Ffn {
+    int n_exp;
+    const int32_t *offsets; // [n_exp + 1]
+    int64_t max_rows;
+    const int32_t *gather;  // or null
+    int d, inter;
+    const uint8_t *x, *xs;  // activations: codes and scales
+    const uint8_t *w[3], *ws[3];
+    uint8_t *h, *hs;        // workspace: codes and scales of H [max_rows][inter]
+    uint16_t *y;            // bf16 [max_rows][d]
+};
+hipError_t launch_mx4_ffn(const Mx4Ffn &a, hipStream_t s);
+
 // ---- dispatch --------------------------------------------------------------
 // Block histogram (64 tokens per block) -> blockcounts[nb][Nr].
 hipError_t launch_perm_hist(const int32_t *topk_idx, int64_t T, int K, int Nr, int32_t *blockcounts,
