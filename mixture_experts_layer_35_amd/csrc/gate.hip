@@ -21,36 +21,43 @@ constexpr int kMaxK = 32;   // slots of a token, at most
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-// Largest of v over the L lanes of a token, in all of them.  Four steps stay inside a row
-// of 16 lanes (DPP); the rest cross rows.
-template <int L, class T, class Op>
-__device__ __forceinline__ T lanes_reduce(T v, Op op) {
-    auto dpp = [](T x, auto ctrl) {
-        const int y = __builtin_bit_cast(int, x);
-        return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(y, y, decltype(ctrl)::value, 0xF, 0xF, false));
+// v combined over the L lanes of a token, in all of them.  Steps inside a row of 16 lanes are DPP
+// moves, the two across rows lane swaps, so no step goes through LDS.
+template <int L, class Op>
+__device__ __forceinline__ uint32_t lanes_reduce(uint32_t v, Op op) {
+    auto dpp = [](uint32_t x, auto ctrl) {
+        return (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, decltype(ctrl)::value, 0xF, 0xF, false);
     };
     v = op(v, dpp(v, std::integral_constant<int, 0xB1>{}));               // lane ^ 1
     v = op(v, dpp(v, std::integral_constant<int, 0x4E>{}));               // lane ^ 2
     if (L >= 8) v = op(v, dpp(v, std::integral_constant<int, 0x141>{}));  // the other quad of 8
     if (L >= 16) v = op(v, dpp(v, std::integral_constant<int, 0x140>{})); // the other half of 16
-    if (L >= 32) v = op(v, __shfl_xor(v, 16, 64));
-    if (L >= 64) v = op(v, __shfl_xor(v, 32, 64));
+    if (L >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = op(r[0], r[1]);
+    }
+    if (L >= 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = op(r[0], r[1]);
+    }
     return v;
-}
-
-template <int L>
-__device__ __forceinline__ float lanes_sum(float v) {
-    return lanes_reduce<L>(v, [](float a, float b) { return a + b; });
-}
-template <int L>
-__device__ __forceinline__ float lanes_max(float v) {
-    return lanes_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 template <int L>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
     return lanes_reduce<L>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
-// fp64 sum of one fp32 value a lane.
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+    return __uint_as_float(lanes_reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }));
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+    return __uint_as_float(lanes_reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
 template <int L>
 __device__ __forceinline__ double lanes_sum(double v) {
 #pragma unroll
@@ -58,10 +65,18 @@ __device__ __forceinline__ double lanes_sum(double v) {
     return v;
 }
 
-// Order of choice values as unsigned integers; 0 stands below all of them.
+// A token's lanes lie in one wave, whose LDS accesses run in order: what they wrote is there for
+// what they read next, and only the compiler has to keep the order.
+__device__ __forceinline__ void token_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Order of choice values (never -0: a score is not) as unsigned integers; 0 stands below all of them.
 __device__ __forceinline__ uint32_t choice_key(float c) {
-    const uint32_t b = __float_as_uint(c == 0.0f ? 0.0f : c);
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    const uint32_t b = __float_as_uint(c);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 constexpr uint32_t kKeyNone = 0x007FFFFFu;   // choice_key(-infinity)
 __device__ __forceinline__ float key_value(uint32_t k) {
@@ -74,6 +89,29 @@ __device__ __forceinline__ float sigmoid_score(float z) { return in_use(z) ? 1.0
 // exp(z - m) of a softmax whose largest logit in use is m (m itself may be +infinity).
 __device__ __forceinline__ float softmax_exp(float z, float m) {
     return !in_use(z) ? 0.0f : z == m ? 1.0f : expf(z - m);
+}
+
+// sigmoid_score of V logits, the same bits.  With r within one ulp of 1/d, r + r (1 - d r) is 1/d
+// correctly rounded (Markstein); tried against the division at every float d >= 1 it fails only above
+// 2^126, where r itself is no normal number.  A third of the division's instructions.
+template <int V>
+__device__ __forceinline__ void sigmoid_scores(const float (&z)[V], float (&s)[V]) {
+    float top = 0.0f;
+#pragma unroll
+    for (int r = 0; r < V; ++r) {
+        s[r] = 1.0f + expf(-(in_use(z[r]) ? z[r] : neg_inf()));
+        top = fmaxf(top, s[r]);
+    }
+    if (__any(top > 0x1p126f)) {
+#pragma unroll
+        for (int r = 0; r < V; ++r) s[r] = 1.0f / s[r];
+    } else {
+#pragma unroll
+        for (int r = 0; r < V; ++r) {
+            const float q = __builtin_amdgcn_rcpf(s[r]);
+            s[r] = __builtin_fmaf(__builtin_fmaf(-s[r], q, 1.0f), q, q);
+        }
+    }
 }
 
 template <int DT>
@@ -130,7 +168,8 @@ struct GateArgs {
     int64_t T, ld, dld;
     int E, G, M, K;
     bool softmax, renorm, group_max;
-    bool vec, svec, dvec;   // rows of the logits, of scores / ds and of dlogits take four-value accesses
+    // whether rows of the logits, of scores / ds, of dlogits and the bias take four-value accesses
+    bool vec, svec, dvec, bvec;
     float scale;
     const void *logits;
     const float *bias;
@@ -142,9 +181,10 @@ struct GateArgs {
     void *dlogits;
 };
 
-// Softmax statistics of a token: largest logit in use and 1 / sum of the exponentials (0 where none is in use).
+// Softmax statistics of a token: the exponentials e, the largest logit in use, and 1 / sum of e (0
+// where no expert is in use).
 template <int L, int V>
-__device__ __forceinline__ void softmax_stats(const float (&z)[V], float &m, float &inv) {
+__device__ __forceinline__ void softmax_stats(const float (&z)[V], float (&e)[V], float &m, float &inv) {
     float t = neg_inf();
 #pragma unroll
     for (int r = 0; r < V; ++r) t = fmaxf(t, z[r]);   // fmaxf passes over NaN
@@ -152,25 +192,32 @@ __device__ __forceinline__ void softmax_stats(const float (&z)[V], float &m, flo
     // the sum is held in 64 bits and rounded once, so that no order of the additions can move a choice
     double sum = 0.0;
 #pragma unroll
-    for (int r = 0; r < V; ++r) sum += softmax_exp(z[r], m);
+    for (int r = 0; r < V; ++r) {
+        e[r] = softmax_exp(z[r], m);
+        sum += e[r];
+    }
     const float total = (float)lanes_sum<L>(sum);
     inv = total > 0.0f ? 1.0f / total : 0.0f;
 }
 
-__host__ __device__ inline int gate_lds_floats(int E, int G) { return 2 * kMaxK + (G > 1 ? E + G : 0); }
-__host__ __device__ inline int gate_backward_lds_floats(int E) { return E + 3; }
+// LDS of a token: the slots' keys and indices, the scores, and with groups the choice values (a
+// group's a word apart from the next one's bank) and the groups' keys.
+__host__ __device__ inline int gate_lds_words(int E, int G) {
+    return 2 * kMaxK + ((E + 3) & ~3) + (G > 1 ? E + 2 * G : 0) + 1;
+}
 
 template <int DT, int L, int V>
 __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs a) {
     constexpr int TPB = kGateThreads / L;                 // tokens per workgroup
-    extern __shared__ float lds[];
-    const int sub = threadIdx.x / L, l = threadIdx.x % L;
+    constexpr int Q = L < kMaxK ? kMaxK / L : 1;          // slots a lane handles, at most
+    extern __shared__ uint32_t lds[];
+    const int sub = threadIdx.x / L, l = threadIdx.x % L, lane = threadIdx.x & 63, base = lane / L * L;
     const int E = a.E, K = a.K, G = a.G;
-    // per token: the slots' keys and indices, then (with groups) the choice values and the groups' keys
-    uint32_t *slot_key = (uint32_t *)(lds + sub * gate_lds_floats(E, G));
+    uint32_t *slot_key = lds + sub * gate_lds_words(E, G);
     int *slot_idx = (int *)(slot_key + kMaxK);
-    float *cval = (float *)(slot_idx + kMaxK);
-    uint32_t *gkey = (uint32_t *)(cval + E);
+    float *sval = (float *)(slot_idx + kMaxK);
+    uint32_t *ckey = (uint32_t *)(sval + ((E + 3) & ~3));
+    uint32_t *gkey = ckey + E + G;
     // the wave's tokens past T work on the last one and store nothing
     const int64_t t0 = (int64_t)blockIdx.x * TPB + sub;
     const bool live = t0 < a.T;
@@ -178,160 +225,198 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs a) {
     const char *row = (const char *)a.logits + t * a.ld * (DT == DT_F32 ? 4 : 2);
     const int i0 = l * V;
 
-    float z[V];
+    float z[V], b[V], s[V];
     load_row<DT, V>(row, i0, E, a.vec, neg_inf(), z);
-    float m = 0.0f, inv = 0.0f;
-    if (a.softmax) softmax_stats<L, V>(z, m, inv);
-    auto score = [&](float x) { return a.softmax ? softmax_exp(x, m) * inv : sigmoid_score(x); };
+    if (a.bias) load_row<DT_F32, V>(a.bias, i0, E, a.bvec, 0.0f, b);
+    if (a.softmax) {
+        float m, inv;
+        softmax_stats<L, V>(z, s, m, inv);
+#pragma unroll
+        for (int r = 0; r < V; ++r) s[r] *= inv;
+    } else {
+        sigmoid_scores<V>(z, s);
+    }
     uint32_t key[V];
-    float s[V];
 #pragma unroll
     for (int r = 0; r < V; ++r) {
-        s[r] = score(z[r]);
-        float c = s[r];
-        if (a.bias) c += i0 + r < E ? a.bias[i0 + r] : 0.0f;
-        if (!in_use(z[r]) || c != c) c = neg_inf();
-        key[r] = i0 + r < E ? choice_key(c) : 0u;
+        const float c = a.bias ? s[r] + b[r] : s[r];
+        // an expert out of use, or whose choice value is NaN, orders as -infinity
+        key[r] = in_use(z[r]) && c == c ? choice_key(c) : kKeyNone;
+        if (i0 + r >= E) key[r] = 0u;
+        if (i0 + r < E) sval[i0 + r] = s[r];
     }
     if (a.scores && live) store_row<DT_F32, V>(a.scores + t * E, i0, E, a.svec, s);
 
     if (G > 1) {
         const int gs = E / G;
+        int g = i0 / gs, left = (g + 1) * gs - i0;
 #pragma unroll
-        for (int r = 0; r < V; ++r)
-            if (i0 + r < E) cval[i0 + r] = key_value(key[r]);
-        __syncthreads();
-        for (int g = l; g < G; g += L) {
-            float v1 = neg_inf(), v2 = neg_inf();
-            for (int i = 0; i < gs; ++i) {
-                const float c = cval[g * gs + i];
-                v2 = fmaxf(v2, fminf(v1, c));
-                v1 = fmaxf(v1, c);
+        for (int r = 0; r < V; ++r) {
+            if (i0 + r < E) ckey[i0 + r + g] = key[r];
+            if (--left == 0) {
+                ++g;
+                left = gs;
             }
-            gkey[g] = choice_key(a.group_max || v2 == neg_inf() ? v1 : v1 + v2);
         }
-        __syncthreads();
+        token_lds_order();
+        // a group's two largest keys, by one lane
+        for (int o = l; o < G; o += L) {
+            uint32_t k1 = 0, k2 = 0;
+            const uint32_t *p = ckey + o * (gs + 1);
+#pragma unroll 8
+            for (int i = 0; i < gs; ++i) {
+                const uint32_t c = p[i];
+                k2 = max(k2, min(k1, c));
+                k1 = max(k1, c);
+            }
+            if (!a.group_max && k2 > kKeyNone) k1 = choice_key(key_value(k1) + key_value(k2));
+            gkey[o] = k1;
+        }
+        token_lds_order();
         // a group is kept when fewer than M others come before it
         uint32_t lo = 0, hi = 0;
-        for (int g = l; g < G; g += L) {
-            const uint32_t k = gkey[g];
+        for (int o = l; o < G; o += L) {
+            const uint32_t k = gkey[o];
             int before = 0;
-            for (int o = 0; o < G; ++o) before += gkey[o] > k || (gkey[o] == k && o < g) ? 1 : 0;
+#pragma unroll 8
+            for (int p = 0; p < G; ++p) before += gkey[p] > k || (gkey[p] == k && p < o) ? 1 : 0;
             if (before < a.M) {
-                if (g < 32) lo |= 1u << g;
-                else hi |= 1u << (g - 32);
+                if (o < 32) lo |= 1u << o;
+                else hi |= 1u << (o - 32);
             }
         }
         auto either = [](uint32_t x, uint32_t y) { return x | y; };
         lo = lanes_reduce<L>(lo, either);
-        hi = lanes_reduce<L>(hi, either);
+        if (G > 32) hi = lanes_reduce<L>(hi, either);
         const uint64_t kept = (uint64_t)hi << 32 | lo;
+        g = i0 / gs;
+        left = (g + 1) * gs - i0;
 #pragma unroll
-        for (int r = 0; r < V; ++r)
-            if (key[r] != 0u && !((kept >> ((i0 + r) / gs)) & 1)) key[r] = kKeyNone;
-    }
-
-    // K rounds: the lane with the largest key (the lowest of them) gives up its first such expert
-    uint32_t best;
-    int at;
-    auto head = [&]() {
-        best = 0;
-        at = 0;
-#pragma unroll
-        for (int r = V - 1; r >= 0; --r) {
-            if (key[r] >= best) {
-                best = key[r];
-                at = r;
+        for (int r = 0; r < V; ++r) {
+            if (!((kept >> (g & 63)) & 1)) key[r] = min(key[r], kKeyNone);
+            if (--left == 0) {
+                ++g;
+                left = gs;
             }
         }
-    };
-    head();
-    const int lane = threadIdx.x & 63, base = lane / L * L;
+    }
+
+    // K rounds: the lane with the largest key (the lowest such lane) gives up its first such expert
     for (int j = 0; j < K; ++j) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int r = 1; r < V; ++r) best = max(best, key[r]);
         const uint32_t top = lanes_max<L>(best);
         const uint64_t who = __ballot(best == top);
-        const int winner = base + __builtin_ctzll(who >> base);
-        if (lane == winner) {
+        if (lane == base + __builtin_ctzll(who >> base)) {
+            int at = 0;
+            bool found = false;
+#pragma unroll
+            for (int r = 0; r < V; ++r) {
+                const bool take = key[r] == top && !found;
+                found = found || take;
+                at = take ? r : at;
+                key[r] = take ? 0u : key[r];
+            }
             slot_key[j] = top;
             slot_idx[j] = i0 + at;
-#pragma unroll
-            for (int r = 0; r < V; ++r)
-                if (r == at) key[r] = 0u;
-            head();
         }
     }
-    __syncthreads();
+    token_lds_order();
     // the slots' weights, and their sum from left to right
-    auto slot_score = [&](int j) {
-        return slot_key[j] == kKeyNone ? 0.0f : score(load1<DT>(row, slot_idx[j]));
-    };
-    constexpr int Q = L < kMaxK ? kMaxK / L : 1;          // slots a lane handles, at most
-    float mine[Q];
+    float w[Q];
+    int ix[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-        const int j = l + q * L;
-        mine[q] = j < K ? slot_score(j) : 0.0f;
+        const int j = min(l + q * L, K - 1);
+        ix[q] = slot_idx[j];
+        w[q] = slot_key[j] == kKeyNone ? 0.0f : sval[ix[q]];
     }
     if (a.renorm) {
-        __syncthreads();
+        token_lds_order();
 #pragma unroll
         for (int q = 0; q < Q; ++q)
-            if (l + q * L < K) slot_key[l + q * L] = __float_as_uint(mine[q]);
-        __syncthreads();
+            if (l + q * L < K) slot_key[l + q * L] = __float_as_uint(w[q]);
+        token_lds_order();
         float total = 0.0f;
+#pragma unroll 8
         for (int j = 0; j < K; ++j) total += __uint_as_float(slot_key[j]);
 #pragma unroll
-        for (int q = 0; q < Q; ++q) mine[q] = total > 0.0f ? mine[q] / total : 0.0f;
+        for (int q = 0; q < Q; ++q) w[q] = total > 0.0f ? w[q] / total : 0.0f;
     }
     if (!live) return;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         const int j = l + q * L;
         if (j < K) {
-            a.idx[t * K + j] = slot_idx[j];
-            a.w[t * K + j] = mine[q] * a.scale;
+            a.idx[t * K + j] = ix[q];
+            a.w[t * K + j] = w[q] * a.scale;
         }
     }
 }
 
-template <int DT, int L, int V>
+__host__ __device__ inline int gate_backward_lds_words(int E) { return ((E + 3) & ~3) + 1; }
+
+// DENSE: softmax scores, or a gradient at every score.  Otherwise only the chosen logits have a
+// gradient, and only they are read.
+template <int DT, int L, int V, bool DENSE>
 __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(const GateArgs a) {
     constexpr int TPB = kGateThreads / L;
-    constexpr int Q = L < kMaxK ? kMaxK / L : 1;          // slots a lane handles, at most
-    extern __shared__ float lds[];
+    constexpr int Q = L < kMaxK ? kMaxK / L : 1;
+    extern __shared__ uint32_t lds[];
     const int sub = threadIdx.x / L, l = threadIdx.x % L;
     const int E = a.E, K = a.K;
-    float *dsl = lds + sub * gate_backward_lds_floats(E); // the slots' part of ds
+    float *dsl = (float *)(lds + sub * gate_backward_lds_words(E));   // the slots' part of ds, or of dz
     const int64_t t0 = (int64_t)blockIdx.x * TPB + sub;
     const bool live = t0 < a.T;
     const int64_t t = live ? t0 : a.T - 1;
     const char *row = (const char *)a.logits + t * a.ld * (DT == DT_F32 ? 4 : 2);
     const int i0 = l * V;
 
-    float z[V], m = 0.0f, inv = 0.0f;
-    load_row<DT, V>(row, i0, E, a.vec, neg_inf(), z);
-    if (a.softmax) softmax_stats<L, V>(z, m, inv);
-    auto score = [&](float x) { return a.softmax ? softmax_exp(x, m) * inv : sigmoid_score(x); };
+    float z[V], d[V], m = 0.0f, inv = 0.0f;
+    int ij[Q];
+    float sj[Q], gj[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const int j = l + q * L;
+        const int64_t at = t * K + min(j, K - 1);
+        const float w = a.cw[at];
+        ij[q] = a.cidx[at];
+        gj[q] = a.dw[at];
+        if (j >= K || w == 0.0f || (unsigned)ij[q] >= (unsigned)E) ij[q] = -1;
+    }
+    const float w0 = a.cw[t * K], dw0 = a.dw[t * K];
+    if (DENSE) {
+        load_row<DT, V>(row, i0, E, a.vec, neg_inf(), z);
+        if (a.ds) load_row<DT_F32, V>(a.ds + t * E, i0, E, a.svec, 0.0f, d);
+    }
+    // the slots' logits; slots without a weight read the first one and do not use it
+#pragma unroll
+    for (int q = 0; q < Q; ++q) sj[q] = load1<DT>(row, max(ij[q], 0));
 #pragma unroll
     for (int r = 0; r < V; ++r)
         if (i0 + r < E) dsl[i0 + r] = 0.0f;
 
-    // slots: s_j and g_j, zero where the weight is 0.  The weights' sum is fixed under
-    // renormalisation, so a common part of the g moves nothing: taking g_0 away first keeps the
-    // difference below exact where the g are alike (K = 1 gives 0).
-    float sj[Q], gj[Q];
-    int ij[Q];
-    const float g0 = a.renorm && a.cw[t * K] != 0.0f ? a.dw[t * K] : 0.0f;
+    float s[V];
+    if (DENSE) {
+        if (a.softmax) {
+            softmax_stats<L, V>(z, s, m, inv);
+#pragma unroll
+            for (int r = 0; r < V; ++r) s[r] *= inv;
+        } else {
+            sigmoid_scores<V>(z, s);
+        }
+    }
+    // Slots: s_j and g_j.  The weights' sum is fixed under renormalisation, so a common part of the g
+    // moves nothing: taking g_0 away first keeps the difference below exact where the g are alike
+    // (K = 1 gives 0).
+    const float g0 = a.renorm && w0 != 0.0f ? dw0 : 0.0f;
     float sum_s = 0.0f, sum_gs = 0.0f;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-        const int j = l + q * L;
-        const bool on = j < K && a.cw[t * K + j] != 0.0f;
-        ij[q] = on ? a.cidx[t * K + j] : 0;
-        const bool ok = on && (unsigned)ij[q] < (unsigned)E;
-        if (!ok) ij[q] = -1;
-        sj[q] = ok ? score(load1<DT>(row, ij[q])) : 0.0f;
-        gj[q] = ok ? a.dw[t * K + j] - g0 : 0.0f;
+        const bool on = ij[q] >= 0;
+        sj[q] = !on ? 0.0f : a.softmax ? softmax_exp(sj[q], m) * inv : sigmoid_score(sj[q]);
+        gj[q] = on ? gj[q] - g0 : 0.0f;
         sum_s += sj[q];
         sum_gs += gj[q] * sj[q];
     }
@@ -341,42 +426,54 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(const GateA
         invd = D > 0.0f ? 1.0f / D : 0.0f;
         mean = lanes_sum<L>(sum_gs) * invd;
     }
-    __syncthreads();
+    token_lds_order();
 #pragma unroll
-    for (int q = 0; q < Q; ++q)
-        if (ij[q] >= 0) dsl[ij[q]] = (gj[q] - mean) * invd * a.scale;
-    __syncthreads();
+    for (int q = 0; q < Q; ++q) {
+        if (ij[q] < 0) continue;
+        const float ds = (gj[q] - mean) * invd * a.scale;
+        dsl[ij[q]] = DENSE ? ds : ds * sj[q] * (1.0f - sj[q]);
+    }
+    token_lds_order();
 
-    float d[V], s[V];
-    if (a.ds) load_row<DT_F32, V>(a.ds + t * E, i0, E, a.svec, 0.0f, d);
-    else {
+    float o[V];
 #pragma unroll
-        for (int r = 0; r < V; ++r) d[r] = 0.0f;
+    for (int r = 0; r < V; ++r) o[r] = i0 + r < E ? dsl[i0 + r] : 0.0f;
+    if (DENSE) {
+        float dot = 0.0f;
+#pragma unroll
+        for (int r = 0; r < V; ++r) {
+            // an expert out of use takes no gradient, whatever the caller's dscores holds there
+            o[r] = in_use(z[r]) ? (a.ds ? d[r] + o[r] : o[r]) : 0.0f;
+            dot += o[r] * s[r];
+        }
+        if (a.softmax) dot = lanes_sum<L>(dot);
+#pragma unroll
+        for (int r = 0; r < V; ++r) o[r] = a.softmax ? s[r] * (o[r] - dot) : o[r] * s[r] * (1.0f - s[r]);
     }
-    float dot = 0.0f;
-#pragma unroll
-    for (int r = 0; r < V; ++r) {
-        s[r] = score(z[r]);
-        // an expert out of use takes no gradient, whatever the caller's dscores holds there
-        d[r] = in_use(z[r]) ? d[r] + (i0 + r < E ? dsl[i0 + r] : 0.0f) : 0.0f;
-        dot += d[r] * s[r];
-    }
-    if (a.softmax) dot = lanes_sum<L>(dot);
-#pragma unroll
-    for (int r = 0; r < V; ++r) d[r] = a.softmax ? s[r] * (d[r] - dot) : d[r] * s[r] * (1.0f - s[r]);
-    if (live) store_row<DT, V>((char *)a.dlogits + t * a.dld * (DT == DT_F32 ? 4 : 2), i0, E, a.dvec, d);
+    if (live) store_row<DT, V>((char *)a.dlogits + t * a.dld * (DT == DT_F32 ? 4 : 2), i0, E, a.dvec, o);
 }
 
-// f(L, V) for the smallest token width that holds E experts: up to 16 values a lane, so that a
-// wave serves four tokens at 256 experts.
+// f(L, V) for a token width that holds E experts.  Up to 16 values a lane keep a wave on four tokens
+// at 256 experts, which costs the fewest instructions a token; a batch whose waves would leave compute
+// units idle takes four values a lane instead, the shortest chain of instructions to its end.
 template <class F>
-hipError_t with_width(int E, F f) {
+hipError_t with_width(int64_t T, int E, F f) {
     using std::integral_constant;
+    const bool few = T * ((E + 3) / 4) <= (int64_t)device_cus() * 4 * 64;   // lanes of 4 values fill one wave a SIMD
     if (E <= 32) return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
     if (E <= 64) return f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
-    if (E <= 128) return f(integral_constant<int, 16>{}, integral_constant<int, 8>{});
-    if (E <= 256) return f(integral_constant<int, 16>{}, integral_constant<int, 16>{});
-    if (E <= 512) return f(integral_constant<int, 32>{}, integral_constant<int, 16>{});
+    if (E <= 128) {
+        if (few) return f(integral_constant<int, 32>{}, integral_constant<int, 4>{});
+        return f(integral_constant<int, 16>{}, integral_constant<int, 8>{});
+    }
+    if (E <= 256) {
+        if (few) return f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+        return f(integral_constant<int, 16>{}, integral_constant<int, 16>{});
+    }
+    if (E <= 512) {
+        if (few) return f(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+        return f(integral_constant<int, 32>{}, integral_constant<int, 16>{});
+    }
     return f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
 }
 
@@ -406,14 +503,15 @@ hipError_t launch_gate(const GateProblem &p, const float *bias, float *scores, i
     if (p.T <= 0) return hipSuccess;
     GateArgs a = gate_args(p);
     a.bias = bias;
+    a.bvec = rows_of_four(bias, 0, 4);
     a.scores = scores;
     a.svec = rows_of_four(scores, p.E, 4);
     a.idx = idx;
     a.w = w;
-    return with_width(p.E, [&](auto lc, auto vc) {
+    return with_width(p.T, p.E, [&](auto lc, auto vc) {
         constexpr int L = decltype(lc)::value, V = decltype(vc)::value, TPB = kGateThreads / L;
         const unsigned grid = (unsigned)((p.T + TPB - 1) / TPB);
-        const size_t lds = (size_t)TPB * gate_lds_floats(p.E, p.G) * 4;
+        const size_t lds = (size_t)TPB * gate_lds_words(p.E, p.G) * 4;
         if (p.dt == DT_F32) gate_kernel<DT_F32, L, V><<<grid, kGateThreads, lds, s>>>(a);
         else gate_kernel<DT_BF16, L, V><<<grid, kGateThreads, lds, s>>>(a);
         return hipGetLastError();
@@ -432,12 +530,18 @@ hipError_t launch_gate_backward(const GateProblem &p, const int32_t *idx, const 
     a.dlogits = dlogits;
     a.dld = dld;
     a.dvec = rows_of_four(dlogits, dld, p.dt == DT_F32 ? 4 : 2);
-    return with_width(p.E, [&](auto lc, auto vc) {
+    return with_width(p.T, p.E, [&](auto lc, auto vc) {
         constexpr int L = decltype(lc)::value, V = decltype(vc)::value, TPB = kGateThreads / L;
         const unsigned grid = (unsigned)((p.T + TPB - 1) / TPB);
-        const size_t lds = (size_t)TPB * gate_backward_lds_floats(p.E) * 4;
-        if (p.dt == DT_F32) gate_backward_kernel<DT_F32, L, V><<<grid, kGateThreads, lds, s>>>(a);
-        else gate_backward_kernel<DT_BF16, L, V><<<grid, kGateThreads, lds, s>>>(a);
+        const size_t lds = (size_t)TPB * gate_backward_lds_words(p.E) * 4;
+        const bool dense = p.softmax || ds;
+        if (p.dt == DT_F32) {
+            if (dense) gate_backward_kernel<DT_F32, L, V, true><<<grid, kGateThreads, lds, s>>>(a);
+            else gate_backward_kernel<DT_F32, L, V, false><<<grid, kGateThreads, lds, s>>>(a);
+        } else {
+            if (dense) gate_backward_kernel<DT_BF16, L, V, true><<<grid, kGateThreads, lds, s>>>(a);
+            else gate_backward_kernel<DT_BF16, L, V, false><<<grid, kGateThreads, lds, s>>>(a);
+        }
         return hipGetLastError();
     });
 }
