@@ -172,7 +172,8 @@ __device__ __forceinline__ f32x16 mx4_mfma(i32x4 a, i32x4 b, f32x16 c, uint32_t 
 }
 
 // The list of tiles: experts in order, an expert's feature tiles, a feature tile's row blocks.  Every
-// wave works with it by itself: lane l adds up the tiles of experts l*P .. l*P + P-1.
+// wave works with it by itself: lane l adds up the tiles of experts l*P .. l*P + P-1.  The offsets lie
+// in LDS, so that looking a tile up does not wait for the loads under way.
 struct TileList {
     const int32_t *offsets;
     int P, bm, ftiles;
@@ -197,7 +198,7 @@ struct TileList {
     __device__ int blocks(int e) const { return (offsets[e + 1] - offsets[e] + bm - 1) / bm; }
     // Tile t < total (the same in all lanes): expert, feature tile, first row and number of rows.  An
     // expert's rows are split evenly over its blocks.
-    __device__ void find(int t, int lane, int &e, int &ft, int64_t &row0, int &valid) const {
+    __device__ void find(int t, int lane, int &e, int &ft, int &row0, int &valid) const {
         const uint64_t started = __ballot(count > 0 && base <= t);
         const int owner = 63 - __builtin_clzll(started);
         int le = 0, rest = t - base;
@@ -216,20 +217,14 @@ struct TileList {
         // quotients are vector instructions: back to scalars, which the descriptors have to be
         ft = __builtin_amdgcn_readfirstlane(rest / mt);
         const int block = rest - ft * mt, mq = __builtin_amdgcn_readfirstlane(m / mt), mr = m - mq * mt;
-        row0 = (int64_t)first + block * mq + min(block, mr);
+        row0 = first + block * mq + min(block, mr);
         valid = mq + (block < mr ? 1 : 0);
     }
 };
 
-// A wave's weight rows, read through buffer descriptors: of each of its two blocks one for the codes and
-// one for the scales, based at the block's first row.  Offsets past a descriptor's bytes read as zero, so
-// a lane without work (kNoOffset) reads zeros at no cost: weights of 0 at a finite scale.
+// Buffer descriptors: offsets past a descriptor's bytes read as zero and are not written, so a lane
+// without work takes kNoOffset.
 constexpr uint32_t kNoOffset = 0x80000000u;
-
-struct Mx4Rows {
-    __amdgpu_buffer_rsrc_t w[2], s[2];
-    uint32_t wo[2], so[2];       // the lane's row and half
-};
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t mx4_rsrc(const uint8_t *p, int64_t bytes) {
     const uint64_t u = (uint64_t)p;
@@ -239,34 +234,51 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t mx4_rsrc(const uint8_t *p, int
                                              0x00020000);
 }
 
-template <bool GATEUP>
-__device__ __forceinline__ Mx4Rows mx4_rows(const Mx4Pass &a, int e, int ft, int lane) {
-    const uint32_t wrow = (uint32_t)a.kruns * 64, srow = (uint32_t)a.kruns * 4;
-    Mx4Rows R;
+// 16-byte piece p of row r in LDS: rows are 128 bytes, and the 16 lanes that LDS serves together (quads
+// of a wave half with the same bit parity) hold each of the eight row pairs' low three bits once, which
+// this permutation turns into eight different pieces.
+__device__ __forceinline__ int mx4_swz(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int mx4_lds(int r, int p) { return r * 128 + ((p ^ mx4_swz(r)) << 4); }
+
+// A wave's 64 weight rows on their way to LDS, a segment at a time: eight loads of 1 KB (8 rows each, whole
+// lines; lane l brings the piece that belongs in place l mod 8 of its row) and two of their scales.
+// Rows past the features, and the half that an odd number of runs lacks, read as zeros.
+constexpr int kMx4WeightBytes = 64 * 128, kMx4WeightLoads = 10;
+
+struct Mx4Weights {
+    __amdgpu_buffer_rsrc_t w[2], s[2];
+    uint32_t wo[8], so[2];
+    template <bool GATEUP>
+    __device__ __forceinline__ void aim(const Mx4Pass &a, int e, int ft, int lane) {
+        const uint32_t wrow = (uint32_t)a.kruns * 64, srow = (uint32_t)a.kruns * 4;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int f0 = GATEUP ? ft * 32 : ft * 64 + i * 32;
-        const int n = max(0, min(32, a.F - f0));       // rows of the block
-        const int64_t r = (int64_t)e * a.F + min(f0, a.F - 1);
-        R.w[i] = mx4_rsrc((GATEUP && i ? a.w1 : a.w0) + r * wrow, (int64_t)n * wrow);
-        R.s[i] = mx4_rsrc((GATEUP && i ? a.s1 : a.s0) + r * srow, (int64_t)n * srow);
-        const bool in = (lane & 31) < n;
-        R.wo[i] = in ? (lane & 31) * wrow + (lane >> 5) * 64 : kNoOffset;
-        R.so[i] = in ? (lane & 31) * srow + (lane >> 5) * 4 : kNoOffset;
+        for (int i = 0; i < 2; ++i) {
+            const int f0 = GATEUP ? ft * 32 : ft * 64 + i * 32;
+            const int n = max(0, min(32, a.F - f0));       // rows of the block
+            const int64_t r = (int64_t)e * a.F + min(f0, a.F - 1);
+            w[i] = mx4_rsrc((GATEUP && i ? a.w1 : a.w0) + r * wrow, (int64_t)n * wrow);
+            s[i] = mx4_rsrc((GATEUP && i ? a.s1 : a.s0) + r * srow, (int64_t)n * srow);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = j * 8 + (lane >> 3);
+                wo[i * 4 + j] = row < n ? (uint32_t)row * wrow + (((lane & 7) ^ mx4_swz(row)) << 4) : kNoOffset;
+            }
+            so[i] = (lane >> 1) < n ? (uint32_t)(lane >> 1) * srow + (lane & 1) * 4 : kNoOffset;
+        }
     }
-    return R;
-}
-
-__device__ __forceinline__ i32x4 mx4_load16(__amdgpu_buffer_rsrc_t r, uint32_t vo, uint32_t so) {
-    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)vo, (int)so, 0));
-}
-__device__ __forceinline__ uint32_t mx4_load4(__amdgpu_buffer_rsrc_t r, uint32_t vo, uint32_t so) {
-    return __builtin_amdgcn_raw_buffer_load_b32(r, (int)vo, (int)so, 0);
-}
-
-// At the end of a loop body whose last loads are for its next round: keeps the compiler from merging them
-// with the loads ahead of the loop into one at the loop's head, right before their use.
-__device__ __forceinline__ void stay_here() { asm volatile("; loads of the next round are under way"); }
+    // segment k to dst (codes, then 512 bytes of scales)
+    __device__ __forceinline__ void load(const Mx4Pass &a, int k, char *dst, int lane) const {
+        const bool tail = 2 * k + 1 == a.kruns;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const bool none = tail && (((lane & 7) ^ mx4_swz((i & 3) * 8 + (lane >> 3))) & 4);
+            buffer_dma16(w[i >> 2], none ? kNoOffset : wo[i], k * 128, dst + i * 1024);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            buffer_dma4(s[i], tail && (lane & 1) ? kNoOffset : so[i], k * 8, dst + kMx4WeightBytes + i * 256);
+    }
+};
 
 // Where a tile's results go: descriptors based at its first row.
 struct Mx4Out {
@@ -350,84 +362,125 @@ __device__ __forceinline__ void mx4_store(const Mx4Pass &a, const Mx4Out &O, con
 constexpr int kMx4Threads = 256;
 constexpr int kMx4Waves = kMx4Threads / 64;
 
-// Few rows an expert: bound by the stream of weights.  Waves take tiles of 64 weight rows and up to 32
-// tokens by themselves, weights and tokens straight from memory to registers, each piece of the next
-// segment requested as soon as this one's has been used.  SPLIT: too few tiles to occupy the GPU; the
-// four waves of a workgroup then share a tile, each a quarter of the segments, and add up in LDS.
+// The offsets in LDS, by the whole workgroup.
+__device__ __forceinline__ void mx4_offsets(const Mx4Pass &a, int32_t *o) {
+    for (int i = threadIdx.x; i <= a.n_exp; i += kMx4Threads) o[i] = a.offsets[i];
+    __syncthreads();
+}
+constexpr int kMx4OffsetBytes = (kMaxExperts + 1 + 63) / 64 * 256;
+
+// Few rows an expert: bound by the stream of weights.  A wave takes tiles of 64 weight rows and up to 32
+// tokens by itself; weights and tokens pass through a ring of segments in LDS that is the wave's own,
+// filled by direct loads and emptied without a barrier, across the ends of tiles.  SPLIT: too few tiles
+// to occupy the GPU; the four waves of a workgroup then share a tile, each a quarter of the segments,
+// and add up in LDS, which leaves room for two segments a wave instead of three.
+constexpr int kMx4SlotBytes = kMx4WeightBytes + 512 + 32 * 128 + 256;
+constexpr int kMx4PartBytes = (kMx4Waves - 1) * 8 * 64 * 16;
+constexpr int mx4_slots(bool split) { return split ? 2 : 3; }
+constexpr int mx4_stream_lds(bool split) {
+    return kMx4OffsetBytes + kMx4Waves * mx4_slots(split) * kMx4SlotBytes + (split ? kMx4PartBytes : 0);
+}
+static_assert(mx4_stream_lds(false) <= 160 * 1024 && mx4_stream_lds(true) <= 160 * 1024, "LDS");
+
 template <bool GATEUP, bool SPLIT>
-__global__ __launch_bounds__(kMx4Threads, 4) void mx4_stream_kernel(const Mx4Pass a) {
-    __shared__ f32x4 part[SPLIT ? (kMx4Waves - 1) * 8 * 64 : 1];
+__global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pass a) {
+    extern __shared__ __align__(16) char smem[];
     const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5, r31 = lane & 31;
+    constexpr int SLOTS = mx4_slots(SPLIT);
+    char *ring = smem + kMx4OffsetBytes + wid * (SLOTS * kMx4SlotBytes);
+    f32x4 *part = (f32x4 *)(smem + kMx4OffsetBytes + kMx4Waves * SLOTS * kMx4SlotBytes);
+    mx4_offsets(a, (int32_t *)smem);
     // gate/up tiles also cover the padding up to whole runs, which is written as zeros
     const int ftiles = GATEUP ? a.hruns * 4 : (a.F + 63) / 64;
     TileList list;
-    list.init(a.offsets, a.n_exp, 32, ftiles, lane);
+    list.init((const int32_t *)smem, a.n_exp, 32, ftiles, lane);
     const int segs = (a.kruns + 1) / 2;   // with an odd number of runs the last one has no second half
-    const bool second = lane >= 32;
     const int k0 = SPLIT ? segs * wid / kMx4Waves : 0, k1 = SPLIT ? segs * (wid + 1) / kMx4Waves : segs;
     const int step = SPLIT ? gridDim.x : gridDim.x * kMx4Waves;
-    for (int t = SPLIT ? blockIdx.x : blockIdx.x * kMx4Waves + wid; t < list.total; t += step) {
-        int e, ft, valid;
-        int64_t row0;
-        list.find(t, lane, e, ft, row0, valid);
-        const Mx4Rows rows = mx4_rows<GATEUP>(a, e, ft, lane);
-        // token columns past the tile's repeat its last one; their results are not used
-        const int64_t R = row0 + min(lane & 31, valid - 1);
-        const int64_t xr = a.gather ? a.gather[R] : R;
-        const uint8_t *xp = a.x + xr * ((int64_t)a.kruns * 64), *xsp = a.xs + xr * ((int64_t)a.kruns * 4);
-        f32x16 acc[2] = {};
-        i32x4 w[2][4], x[4];
-        uint32_t ws[2], xs, wo[2], so[2];
-        const uint8_t *xk, *xsk;
-        // where segment k lies; a segment past the end reads nothing (tokens: the last one again)
-        auto aim = [&](int k) {
-            const bool none = k >= k1 || (2 * k + 1 == a.kruns && second);
+    const int first = SPLIT ? blockIdx.x : blockIdx.x * kMx4Waves + wid;
+
+    // the tile and segment whose loads are issued next
+    Mx4Weights W;
+    const uint8_t *xp[4], *xsp;
+    int it = first, ik = k0, nx = 0;
+    auto next_tile = [&]() {
+        int e, ft, row0, valid;
+        list.find(it, lane, e, ft, row0, valid);
+        W.aim<GATEUP>(a, e, ft, lane);
+        // token rows past the tile's repeat its last one; their results are not used
+        auto token = [&](int r) {
+            const int64_t R = row0 + min(r, valid - 1);
+            return a.gather ? (int64_t)a.gather[R] : R;
+        };
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                wo[i] = none ? kNoOffset : rows.wo[i];
-                so[i] = none ? kNoOffset : rows.so[i];
-            }
-            const int kx = 2 * min(k, k1 - 1) + (second && 2 * k + 1 < a.kruns ? 1 : 0);
-            xk = xp + (int64_t)kx * 64;
-            xsk = xsp + (int64_t)kx * 4;
-        };
-        auto piece = [&](int k, int c) {
-            w[0][c] = mx4_load16(rows.w[0], wo[0] + c * 16, k * 128);
-            w[1][c] = mx4_load16(rows.w[1], wo[1] + c * 16, k * 128);
-            x[c] = *(const i32x4 *)(xk + c * 16);
-        };
-        auto scales = [&](int k) {
-            ws[0] = mx4_load4(rows.s[0], so[0], k * 8);
-            ws[1] = mx4_load4(rows.s[1], so[1], k * 8);
-            xs = *(const uint32_t *)xsk;
-        };
-        if (k0 < k1) {
-            aim(k0);
-            scales(k0);
+        for (int j = 0; j < 4; ++j) xp[j] = a.x + token(j * 8 + (lane >> 3)) * ((int64_t)a.kruns * 64);
+        xsp = a.xs + token(lane >> 1) * ((int64_t)a.kruns * 4);
+        nx = (valid + 7) >> 3;
+    };
+    // issues the next segment into a slot; the number of loads
+    auto issue = [&](int slot) {
+        if (it >= list.total || k0 >= k1) return 0;
+        if (ik == k0) next_tile();
+        char *dst = ring + slot * kMx4SlotBytes;
+        W.load(a, ik, dst, lane);
+        const bool tail = 2 * ik + 1 == a.kruns;
+        char *xd = dst + kMx4WeightBytes + 512;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) piece(k0, c);
+        for (int j = 0; j < 4; ++j) {
+            // the half that an odd number of runs lacks meets weights of zero: it repeats the other
+            const int p = (lane & 7) ^ mx4_swz(j * 8 + (lane >> 3));
+            if (j < nx) dma16(xp[j] + (int64_t)ik * 128 + (tail ? p & 3 : p) * 16, xd + j * 1024);
         }
+        dma4(xsp + (int64_t)ik * 8 + (tail ? 0 : (lane & 1) * 4), xd + 4096);
+        const int n = kMx4WeightLoads + nx + 1;
+        if (++ik == k1) {
+            ik = k0;
+            it += step;
+        }
+        return n;
+    };
+    // loads of the last segments issued
+    int n1 = 0, n2;
+    issue(0);
+    if (SLOTS > 2) n1 = issue(1);
+    n2 = issue(SLOTS - 1);
+    int slot = 0;
+    for (int t = first; t < list.total; t += step) {
+        f32x16 acc[2] = {};
         for (int k = k0; k < k1; ++k) {
-            const uint32_t us[2] = {ws[0], ws[1]}, vs = xs;
-            aim(k + 1);
-            scales(k + 1);
-            auto step = [&](auto sc) {
-                constexpr int S = decltype(sc)::value;
-                // the order is fixed: a piece's registers are free for the next one once its products are issued
-                __builtin_amdgcn_sched_barrier(0);
-                acc[0] = mx4_mfma<S>(w[0][S], x[S], acc[0], us[0], vs);
-                acc[1] = mx4_mfma<S>(w[1][S], x[S], acc[1], us[1], vs);
-                __builtin_amdgcn_sched_barrier(0);
-                piece(k + 1, S);
-            };
-            step(std::integral_constant<int, 0>{});
-            step(std::integral_constant<int, 1>{});
-            step(std::integral_constant<int, 2>{});
-            step(std::integral_constant<int, 3>{});
-            stay_here();
+            // the segment's own loads are done once only the later segments' are outstanding
+            wait_vmcnt_dyn(n1 + n2);
+            asm volatile("" ::: "memory");
+            const char *src = ring + slot * kMx4SlotBytes;
+            const char *xs0 = src + kMx4WeightBytes + 512;
+            i32x4 w[2][4], x[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                w[0][c] = *(const i32x4 *)(src + mx4_lds(r31, half * 4 + c));
+                w[1][c] = *(const i32x4 *)(src + 4096 + mx4_lds(r31, half * 4 + c));
+                x[c] = *(const i32x4 *)(xs0 + mx4_lds(r31, half * 4 + c));
+            }
+            const uint32_t ws0 = *(const uint32_t *)(src + kMx4WeightBytes + (r31 * 2 + half) * 4);
+            const uint32_t ws1 = *(const uint32_t *)(src + kMx4WeightBytes + 256 + (r31 * 2 + half) * 4);
+            const uint32_t xs = *(const uint32_t *)(xs0 + 4096 + (r31 * 2 + half) * 4);
+            wait_lgkm0();                  // the slot has been read: it can be filled again
+            asm volatile("" ::: "memory");
+            const int n = issue(slot);
+            if (SLOTS > 2) n1 = n2;
+            n2 = n;
+            acc[0] = mx4_mfma<0>(w[0][0], x[0], acc[0], ws0, xs);
+            acc[1] = mx4_mfma<0>(w[1][0], x[0], acc[1], ws1, xs);
+            acc[0] = mx4_mfma<1>(w[0][1], x[1], acc[0], ws0, xs);
+            acc[1] = mx4_mfma<1>(w[1][1], x[1], acc[1], ws1, xs);
+            acc[0] = mx4_mfma<2>(w[0][2], x[2], acc[0], ws0, xs);
+            acc[1] = mx4_mfma<2>(w[1][2], x[2], acc[1], ws1, xs);
+            acc[0] = mx4_mfma<3>(w[0][3], x[3], acc[0], ws0, xs);
+            acc[1] = mx4_mfma<3>(w[1][3], x[3], acc[1], ws1, xs);
+            slot = slot == SLOTS - 1 ? 0 : slot + 1;
         }
         if (SPLIT) {
-            __syncthreads();   // the previous tile's sums have been read
+            cta_barrier();   // the previous tile's sums have been read
             if (wid > 0) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -436,7 +489,8 @@ __global__ __launch_bounds__(kMx4Threads, 4) void mx4_stream_kernel(const Mx4Pas
                         part[((wid - 1) * 8 + i * 4 + q) * 64 + lane] =
                             f32x4{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]};
             }
-            __syncthreads();
+            wait_lgkm0();
+            cta_barrier();
             if (wid > 0) continue;
 #pragma unroll 1
             for (int o = 0; o < kMx4Waves - 1; ++o)
@@ -449,188 +503,133 @@ __global__ __launch_bounds__(kMx4Threads, 4) void mx4_stream_kernel(const Mx4Pas
                         for (int k = 0; k < 4; ++k) acc[i][4 * q + k] += v[k];
                     }
         }
-        mx4_store<GATEUP>(a, mx4_out<GATEUP>(a, row0, valid), acc[0], acc[1], ft, lane & 31, lane);
+        int e, ft, row0, valid;
+        list.find(t, lane, e, ft, row0, valid);
+        mx4_store<GATEUP>(a, mx4_out<GATEUP>(a, row0, valid), acc[0], acc[1], ft, r31, lane);
     }
 }
 
 // Many rows an expert.  A workgroup's tile is 256 weight rows (64 a wave) against up to 256 tokens, one
-// workgroup a compute unit: a wave then has the registers for 64 x 256 sums, two segments of
-// weights on their way and the next step's tokens.  Weights go straight to the registers of the one wave
-// that uses them; the tokens' segments, which all four waves use, pass through two LDS buffers.
+// workgroup a compute unit, so that a wave has the registers for 64 x 256 sums.  Segments pass through a
+// ring of stages in LDS, each wave's weight rows for itself and the tokens for all; the fewer token
+// blocks a tile has, the more stages fit.
 constexpr int kMx4TileTokens = 256;
-
-// 16-byte piece p of token row r in LDS: rows are 128 bytes, and the 16 lanes that LDS serves
-// together (quads of a wave half with the same bit parity) hold each of the eight row
-// pairs' low three bits once, which this permutation turns into eight different pieces.
-__device__ __forceinline__ int mx4_lds(int r, int p) { return r * 128 + ((p ^ ((r >> 1) & 7)) << 4); }
+constexpr int kMx4TileRing = 160 * 1024 - kMx4OffsetBytes;
+// a stage: four waves' weights, then the tokens' codes and scales
+constexpr int mx4_stage_bytes(int tb) { return kMx4Waves * (kMx4WeightBytes + 512) + tb * (32 * 128 + 256); }
 
 template <bool GATEUP>
 __global__ __launch_bounds__(kMx4Threads, 1) void mx4_tile_kernel(const Mx4Pass a) {
-    __shared__ __align__(16) char xbuf[2][kMx4TileTokens * 128];
-    __shared__ uint32_t sbuf[2][kMx4TileTokens * 2];
+    extern __shared__ __align__(16) char smem[];
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = lane >> 5, r31 = lane & 31;
+    char *ring = smem + kMx4OffsetBytes;
+    mx4_offsets(a, (int32_t *)smem);
     const int wtiles = GATEUP ? a.hruns * 4 : (a.F + 63) / 64;
     const int ftiles = (wtiles + kMx4Waves - 1) / kMx4Waves;
     TileList list;
-    list.init(a.offsets, a.n_exp, kMx4TileTokens, ftiles, lane);
+    list.init((const int32_t *)smem, a.n_exp, kMx4TileTokens, ftiles, lane);
     const int segs = (a.kruns + 1) / 2;   // with an odd number of runs the last one has no second half
     // workgroup b runs on XCD b mod 8: each XCD takes a contiguous eighth of the list, so that the row
     // blocks of a weight tile and the weight tiles of a row block meet in its L2
     const int per = (list.total + 7) / 8, xcd = blockIdx.x & 7;
     const int end = min(list.total, (xcd + 1) * per);
-    const int64_t xrow = (int64_t)a.kruns * 64;
 
-    // staging: lane l of wave w brings piece l mod 8 of token rows 32 i + 8 w + l / 8
-    const int srow = wid * 8 + (lane >> 3), sp = lane & 7;
-    struct Tile {
-        Mx4Rows rows;
-        const uint8_t *xp[8], *xsp;
-        int64_t row0;
-        int valid, wt;
-    } T;
-    i32x4 w[2][2][4], xv[8];
-    uint32_t ws[2][2], xsv[2], wo[2], so[2];
-    auto setup = [&](int t) {
-        int e, ft;
-        list.find(t, lane, e, ft, T.row0, T.valid);
-        T.wt = ft * kMx4Waves + wid;
-        T.rows = mx4_rows<GATEUP>(a, e, T.wt, lane);
-        // token rows past the tile's repeat its last one; their results are not used
+    for (int t = xcd * per + (blockIdx.x >> 3); t < end; t += gridDim.x >> 3) {
+        int e, ft, row0, valid;
+        list.find(t, lane, e, ft, row0, valid);
+        const int wt = ft * kMx4Waves + wid;
+        Mx4Weights W;
+        W.aim<GATEUP>(a, e, wt, lane);
+        // token row r of the tile; rows past the tile's repeat its last one, their results are not used
         auto token = [&](int r) {
-            const int64_t R = T.row0 + min(r, T.valid - 1);
+            const int64_t R = row0 + min(r, valid - 1);
             return a.gather ? (int64_t)a.gather[R] : R;
         };
-#pragma unroll
-        for (int i = 0; i < 8; ++i) T.xp[i] = a.x + token(32 * i + srow) * xrow;
-        T.xsp = a.xs + token(tid) * (xrow >> 4);
-    };
-    // (blocks of 32 token rows past the tile's are neither read nor written)
-    auto fetch = [&](int k, auto tbc) {
-        const int last = min(k, segs - 1);
-        // the half that an odd number of runs lacks meets weights of zero: it repeats the other
-        const int64_t o = (int64_t)last * 128 + (2 * last + 1 < a.kruns ? sp : sp & 3) * 16;
-#pragma unroll
-        for (int i = 0; i < decltype(tbc)::value; ++i) xv[i] = *(const i32x4 *)(T.xp[i] + o);
-        const uint8_t *s = T.xsp + (int64_t)last * 8;
-        xsv[0] = *(const uint32_t *)s;
-        xsv[1] = *(const uint32_t *)(s + (2 * last + 1 < a.kruns ? 4 : 0));
-    };
-    auto keep = [&](int k, auto tbc) {
-#pragma unroll
-        for (int i = 0; i < decltype(tbc)::value; ++i) *(i32x4 *)(xbuf[k & 1] + mx4_lds(32 * i + srow, sp)) = xv[i];
-        *(u32x2 *)(sbuf[k & 1] + 2 * tid) = u32x2{xsv[0], xsv[1]};
-    };
-    auto aim = [&](int k) {
-        const bool none = k >= segs || (2 * k + 1 == a.kruns && half);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            wo[i] = none ? kNoOffset : T.rows.wo[i];
-            so[i] = none ? kNoOffset : T.rows.so[i];
-        }
-    };
-    auto piece = [&](int k, int g, int c) {
-        w[g][0][c] = mx4_load16(T.rows.w[0], wo[0] + c * 16, k * 128);
-        w[g][1][c] = mx4_load16(T.rows.w[1], wo[1] + c * 16, k * 128);
-    };
-    auto scales = [&](int k, int g) {
-        ws[g][0] = mx4_load4(T.rows.s[0], so[0], k * 8);
-        ws[g][1] = mx4_load4(T.rows.s[1], so[1], k * 8);
-    };
-    // the loads of a tile's first segments (of all its token rows: the tile's own loop is not chosen yet)
-    auto start = [&](int t) {
-        setup(t);
-        fetch(0, std::integral_constant<int, 8>{});
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            aim(g);
-            scales(g, g);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) piece(g, g, c);
-        }
-    };
-
-    int t = xcd * per + (blockIdx.x >> 3);
-    if (t >= end) return;
-    start(t);
-    // One tile of up to 32 TB tokens.  Segment k's tokens are in LDS buffer k mod 2 and its weights in register
-    // set k mod 2.  Meanwhile segment k + 1's tokens come in, and as a piece's products are issued, that of
-    // segment k + 2; the next tile's first loads are under way while this one's results are written.
-    auto tile = [&](auto tbc) {
-        constexpr int TB = decltype(tbc)::value;
-        f32x16 acc[2][TB] = {};
-        keep(0, tbc);
-        wait_lgkm0();
-        cta_barrier();
-        i32x4 b[2][TB];
-        uint32_t xs[TB];
-        auto tokens = [&](int k, int g, int s) {
+        auto tile = [&](auto tbc) {
+            constexpr int TB = decltype(tbc)::value;
+            constexpr int STAGE = mx4_stage_bytes(TB), S = kMx4TileRing / STAGE < 4 ? kMx4TileRing / STAGE : 4;
+            constexpr int XO = kMx4Waves * (kMx4WeightBytes + 512);     // tokens within a stage
+            constexpr int XS = (TB + kMx4Waves - 1) / kMx4Waves;        // 256-byte loads of token scales a wave
+            constexpr int N = kMx4WeightLoads + TB + XS;                // loads a wave and segment
+            static_assert(S >= 2 && N * (S - 2) < 64, "ring");
+            // the wave brings token rows 8 (4 j + wid) + 0..7, j < TB, and the scales of rows 32 (4 j + wid) + 0..31
+            // (past the last block those of the last again)
+            const uint8_t *xp[TB], *xsp[XS];
 #pragma unroll
             for (int j = 0; j < TB; ++j)
-                b[g][j] = *(const i32x4 *)(xbuf[k & 1] + mx4_lds(j * 32 + r31, half * 4 + s));
-        };
-        auto token_scales = [&](int k) {
+                xp[j] = a.x + token((j * 4 + wid) * 8 + (lane >> 3)) * ((int64_t)a.kruns * 64);
 #pragma unroll
-            for (int j = 0; j < TB; ++j) xs[j] = sbuf[k & 1][(j * 32 + r31) * 2 + half];
-        };
-        tokens(0, 0, 0);
-        token_scales(0);
-        auto segment = [&](int k, auto gc) {
-            constexpr int G = decltype(gc)::value;
-            fetch(k + 1, tbc);
-            const uint32_t us[2] = {ws[G][0], ws[G][1]};
-            uint32_t vs[TB];
-#pragma unroll
-            for (int j = 0; j < TB; ++j) vs[j] = xs[j];
-            aim(k + 2);
-            auto step = [&](auto sc) {
-                constexpr int S = decltype(sc)::value;
-                if (S < 3) {
-                    tokens(k, (S + 1) & 1, S + 1);
-                } else {
-                    // every read of the other buffer's last segment came before the previous barrier
-                    keep(k + 1, tbc);
-                    wait_lgkm0();
-                    cta_barrier();
-                    tokens(k + 1, 0, 0);
-                    token_scales(k + 1);
-                    scales(k + 2, G);
-                }
-                __builtin_amdgcn_sched_barrier(0);
+            for (int j = 0; j < XS; ++j)
+                xsp[j] = a.xs + token(min(j * 4 + wid, TB - 1) * 32 + (lane >> 1)) * ((int64_t)a.kruns * 4);
+            auto issue = [&](int k, char *st) {
+                W.load(a, k, st + wid * (kMx4WeightBytes + 512), lane);
+                const bool tail = 2 * k + 1 == a.kruns;
+                char *xd = st + XO;
 #pragma unroll
                 for (int j = 0; j < TB; ++j) {
-                    acc[0][j] = mx4_mfma<S>(w[G][0][S], b[S & 1][j], acc[0][j], us[0], vs[j]);
-                    acc[1][j] = mx4_mfma<S>(w[G][1][S], b[S & 1][j], acc[1][j], us[1], vs[j]);
+                    // the half that an odd number of runs lacks meets weights of zero: it repeats the other
+                    const int p = (lane & 7) ^ mx4_swz((j * 4 + wid) * 8 + (lane >> 3));
+                    dma16(xp[j] + (int64_t)k * 128 + (tail ? p & 3 : p) * 16, xd + (j * 4 + wid) * 1024);
                 }
-                __builtin_amdgcn_sched_barrier(0);
-                piece(k + 2, G, S);
-            };
-            step(std::integral_constant<int, 0>{});
-            step(std::integral_constant<int, 1>{});
-            step(std::integral_constant<int, 2>{});
-            step(std::integral_constant<int, 3>{});
-        };
-        int k = 0;
-        for (; k + 1 < segs; k += 2) {
-            segment(k, std::integral_constant<int, 0>{});
-            segment(k + 1, std::integral_constant<int, 1>{});
-            stay_here();
-        }
-        if (k < segs) segment(k, std::integral_constant<int, 0>{});
-        const Mx4Out out = mx4_out<GATEUP>(a, T.row0, T.valid);
-        const int wt = T.wt;
-        t += gridDim.x >> 3;
-        cta_barrier();   // every wave is done with the buffers
-        if (t < end) start(t);
-        if (wt < wtiles) {
 #pragma unroll
-            for (int j = 0; j < TB; ++j) mx4_store<GATEUP>(a, out, acc[0][j], acc[1][j], wt, j * 32 + r31, lane);
-        }
-    };
-    while (t < end) {
-        if (T.valid <= 64) tile(std::integral_constant<int, 2>{});
-        else if (T.valid <= 128) tile(std::integral_constant<int, 4>{});
-        else if (T.valid <= 192) tile(std::integral_constant<int, 6>{});
+                for (int j = 0; j < XS; ++j)
+                    dma4(xsp[j] + (int64_t)k * 8 + (tail ? 0 : (lane & 1) * 4),
+                         xd + TB * 4096 + min(j * 4 + wid, TB - 1) * 256);
+            };
+            f32x16 acc[2][TB] = {};
+            cta_barrier();   // every wave is done with the ring
+            for (int k = 0; k < S - 1 && k < segs; ++k) issue(k, ring + k * STAGE);
+            int slot = 0;
+            for (int k = 0; k < segs; ++k) {
+                // the wave's own loads of segment k are done; after the barrier everyone's are, and everyone has
+                // read segment k - 1, whose stage takes segment k + S - 1
+                if (k + S - 1 <= segs) wait_vmcnt<N * (S - 2)>();
+                else wait_vmcnt<0>();
+                cta_barrier();
+                const char *st = ring + slot * STAGE;
+                if (k + S - 1 < segs) issue(k + S - 1, ring + (slot == 0 ? S - 1 : slot - 1) * STAGE);
+                const char *ws = st + wid * (kMx4WeightBytes + 512), *xb = st + XO;
+                uint32_t us[2], vs[TB];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    us[i] = *(const uint32_t *)(ws + kMx4WeightBytes + i * 256 + (r31 * 2 + half) * 4);
+#pragma unroll
+                for (int j = 0; j < TB; ++j) vs[j] = *(const uint32_t *)(xb + TB * 4096 + j * 256 + (r31 * 2 + half) * 4);
+                i32x4 w[2][2], b[2][TB];
+                auto read = [&](int g, int c) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) w[g][i] = *(const i32x4 *)(ws + i * 4096 + mx4_lds(r31, half * 4 + c));
+#pragma unroll
+                    for (int j = 0; j < TB; ++j) b[g][j] = *(const i32x4 *)(xb + mx4_lds(j * 32 + r31, half * 4 + c));
+                };
+                read(0, 0);
+                auto step = [&](auto sc) {
+                    constexpr int C = decltype(sc)::value;
+                    if (C < 3) read((C + 1) & 1, C + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int j = 0; j < TB; ++j) {
+                        acc[0][j] = mx4_mfma<C>(w[C & 1][0], b[C & 1][j], acc[0][j], us[0], vs[j]);
+                        acc[1][j] = mx4_mfma<C>(w[C & 1][1], b[C & 1][j], acc[1][j], us[1], vs[j]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                };
+                step(std::integral_constant<int, 0>{});
+                step(std::integral_constant<int, 1>{});
+                step(std::integral_constant<int, 2>{});
+                step(std::integral_constant<int, 3>{});
+                slot = slot == S - 1 ? 0 : slot + 1;
+            }
+            if (wt < wtiles) {
+                const Mx4Out out = mx4_out<GATEUP>(a, row0, valid);
+#pragma unroll
+                for (int j = 0; j < TB; ++j) mx4_store<GATEUP>(a, out, acc[0][j], acc[1][j], wt, j * 32 + r31, lane);
+            }
+        };
+        if (valid <= 64) tile(std::integral_constant<int, 2>{});
+        else if (valid <= 128) tile(std::integral_constant<int, 4>{});
+        else if (valid <= 192) tile(std::integral_constant<int, 6>{});
         else tile(std::integral_constant<int, 8>{});
     }
 }
@@ -697,24 +696,25 @@ hipError_t launch_mx4_ffn(const Mx4Ffn &a, hipStream_t s) {
     down.y = a.y;
     down.yvec = (uintptr_t)a.y % 16 == 0 && a.d % 8 == 0;
     const int64_t cus = device_cus();
+    const unsigned grid = (unsigned)((cus + 7) / 8 * 8);
+    auto go = [&](auto kernel, int lds, const Mx4Pass &p) {
+        const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+        kernel<<<grid, kMx4Threads, lds, s>>>(p);
+        return hipGetLastError();
+    };
     // 32 rows an expert fill one token block: up to there a tile is bound by its weights
-    if (a.max_rows <= 32 * (int64_t)a.n_exp) {
-        // with fewer tiles than resident waves, at most, a tile takes four waves
-        const int64_t experts = a.max_rows < a.n_exp ? a.max_rows : a.n_exp;
-        const unsigned grid = (unsigned)(4 * cus);
-        auto go = [&](auto gateup, const Mx4Pass &p, int64_t ftiles) {
-            constexpr bool GU = decltype(gateup)::value;
-            if (experts * ftiles < 16 * cus) mx4_stream_kernel<GU, true><<<grid, kMx4Threads, 0, s>>>(p);
-            else mx4_stream_kernel<GU, false><<<grid, kMx4Threads, 0, s>>>(p);
-        };
-        go(std::true_type{}, up, up.hruns * 4);
-        go(std::false_type{}, down, (a.d + 63) / 64);
-    } else {
-        const unsigned grid = (unsigned)((cus + 7) / 8 * 8);
-        mx4_tile_kernel<true><<<grid, kMx4Threads, 0, s>>>(up);
-        mx4_tile_kernel<false><<<grid, kMx4Threads, 0, s>>>(down);
-    }
-    return hipGetLastError();
+    const bool few = a.max_rows <= 32 * (int64_t)a.n_exp;
+    // with fewer tiles than resident waves, at most, a tile takes four waves
+    const int64_t experts = a.max_rows < a.n_exp ? a.max_rows : a.n_exp;
+    auto pass = [&](auto gateup, const Mx4Pass &p, int64_t tiles) {
+        constexpr bool GU = decltype(gateup)::value;
+        if (!few) return go(mx4_tile_kernel<GU>, 160 * 1024, p);
+        if (experts * tiles < 4 * cus) return go(mx4_stream_kernel<GU, true>, mx4_stream_lds(true), p);
+        return go(mx4_stream_kernel<GU, false>, mx4_stream_lds(false), p);
+    };
+    const hipError_t e = pass(std::true_type{}, up, up.hruns * 4);
+    return e != hipSuccess ? e : pass(std::false_type{}, down, (a.d + 63) / 64);
 }
 
 }  // namespace moe
