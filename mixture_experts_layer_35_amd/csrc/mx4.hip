@@ -172,15 +172,15 @@ __device__ __forceinline__ f32x16 mx4_mfma(i32x4 a, i32x4 b, f32x16 c, uint32_t 
 }
 
 // The list of tiles: experts in order, an expert's feature tiles, a feature tile's row blocks.  Every
-// wave works with it by itself: lane l adds up the tiles of experts l*P .. l*P + P-1.  The offsets lie
-// in LDS, so that looking a tile up does not wait for the loads under way.
+// wave works with it by itself: lane l adds up the tiles of experts l*P .. l*P + P-1.  The experts' ends
+// (offsets[1] on) lie in LDS, so that looking a tile up does not wait for the loads under way.
 struct TileList {
-    const int32_t *offsets;
+    const int32_t *ends;
     int P, bm, ftiles;
     int base, count;             // this lane's first tile and tiles
     int total;
     __device__ void init(const int32_t *o, int n, int bm_, int ftiles_, int lane) {
-        offsets = o;
+        ends = o;
         bm = bm_;
         ftiles = ftiles_;
         P = (n + 63) / 64;
@@ -195,7 +195,8 @@ struct TileList {
         base = run - count;
         total = __builtin_amdgcn_readlane(run, 63);
     }
-    __device__ int blocks(int e) const { return (offsets[e + 1] - offsets[e] + bm - 1) / bm; }
+    __device__ int start(int e) const { return e ? ends[e - 1] : 0; }
+    __device__ int blocks(int e) const { return (ends[e] - start(e) + bm - 1) / bm; }
     // Tile t < total (the same in all lanes): expert, feature tile, first row and number of rows.  An
     // expert's rows are split evenly over its blocks.
     __device__ void find(int t, int lane, int &e, int &ft, int &row0, int &valid) const {
@@ -211,8 +212,8 @@ struct TileList {
         }
         e = __builtin_amdgcn_readlane(le, owner);
         rest = __builtin_amdgcn_readlane(rest, owner);
-        const int first = __builtin_amdgcn_readfirstlane(offsets[e]);
-        const int m = __builtin_amdgcn_readfirstlane(offsets[e + 1]) - first;
+        const int first = __builtin_amdgcn_readfirstlane(start(e));
+        const int m = __builtin_amdgcn_readfirstlane(ends[e]) - first;
         const int mt = (m + bm - 1) / bm;
         // quotients are vector instructions: back to scalars, which the descriptors have to be
         ft = __builtin_amdgcn_readfirstlane(rest / mt);
@@ -221,6 +222,10 @@ struct TileList {
         valid = mq + (block < mr ? 1 : 0);
     }
 };
+
+// Keeps products where they are written: without it the compiler moves them behind the reads and barriers that they
+// are meant to run beside.
+__device__ __forceinline__ void mx4_pin(f32x16 &a) { asm volatile("" : "+v"(a)); }
 
 // Buffer descriptors: offsets past a descriptor's bytes read as zero and are not written, so a lane
 // without work takes kNoOffset.
@@ -241,10 +246,17 @@ __device__ __forceinline__ int mx4_swz(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int mx4_lds(int r, int p) { return r * 128 + ((p ^ mx4_swz(r)) << 4); }
 
 // A wave's 64 weight rows on their way to LDS, a segment at a time: eight loads of 1 KB (8 rows each, whole
-// lines; lane l brings the piece that belongs in place l mod 8 of its row) and two of their scales.
-// Rows past the features, and the half that an odd number of runs lacks, read as zeros.
-constexpr int kMx4WeightBytes = 64 * 128, kMx4WeightLoads = 10;
+// lines; lane l brings the piece that belongs in place l mod 8 of its row).  Rows past the features, and the
+// half that an odd number of runs lacks, read as zeros.
+//
+// Scales: a row's eight bytes of a segment are a small part of a line, and every row is another line.  Where
+// rows of scales are whole 16-byte pieces (WIDE: 512 values, aligned), one load brings 16 bytes a row, of two
+// segments; otherwise two loads bring a segment's words, 32 rows each.  (Loading words for every segment made half
+// of all requests to L2: 5.0 TB/s of weights in a copy to LDS against 6.2 without scales.)
+constexpr int kMx4WeightBytes = 64 * 128;
+constexpr int mx4_scale_bytes(bool wide) { return wide ? 16 : 8; }   // of a row, in one slot of scales
 
+template <bool WIDE>
 struct Mx4Weights {
     __amdgpu_buffer_rsrc_t w[2], s[2];
     uint32_t wo[8], so[2];
@@ -263,20 +275,27 @@ struct Mx4Weights {
                 const int row = j * 8 + (lane >> 3);
                 wo[i * 4 + j] = row < n ? (uint32_t)row * wrow + (((lane & 7) ^ mx4_swz(row)) << 4) : kNoOffset;
             }
-            so[i] = (lane >> 1) < n ? (uint32_t)(lane >> 1) * srow + (lane & 1) * 4 : kNoOffset;
+            const int row = WIDE ? lane & 31 : lane >> 1;
+            so[i] = row < n ? (uint32_t)row * srow + (WIDE ? 0 : (lane & 1) * 4) : kNoOffset;
         }
     }
-    // segment k to dst (codes, then 512 bytes of scales)
+    // codes of segment k
     __device__ __forceinline__ void load(const Mx4Pass &a, int k, char *dst, int lane) const {
         const bool tail = 2 * k + 1 == a.kruns;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool none = tail && (((lane & 7) ^ mx4_swz((i & 3) * 8 + (lane >> 3))) & 4);
-            buffer_dma16(w[i >> 2], none ? kNoOffset : wo[i], k * 128, dst + i * 1024);
+        for (int q = 0; q < 8; ++q) {
+            const bool none = tail && (((lane & 7) ^ mx4_swz((q & 3) * 8 + (lane >> 3))) & 4);
+            buffer_dma16(w[q >> 2], none ? kNoOffset : wo[q], k * 128, dst + q * 1024);
         }
+    }
+    // scales of segment k, or (WIDE) of segments k and k + 1; two loads
+    __device__ __forceinline__ void load_scales(const Mx4Pass &a, int k, char *dst, int lane) const {
+        const bool tail = 2 * k + 1 == a.kruns;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            buffer_dma4(s[i], tail && (lane & 1) ? kNoOffset : so[i], k * 8, dst + kMx4WeightBytes + i * 256);
+        for (int i = 0; i < 2; ++i) {
+            if (!WIDE) buffer_dma4(s[i], tail && (lane & 1) ? kNoOffset : so[i], k * 8, dst + i * 256);
+            else if (lane < 32) buffer_dma16(s[i], so[i], k * 8, dst + i * 512);
+        }
     }
 };
 
@@ -362,52 +381,57 @@ __device__ __forceinline__ void mx4_store(const Mx4Pass &a, const Mx4Out &O, con
 constexpr int kMx4Threads = 256;
 constexpr int kMx4Waves = kMx4Threads / 64;
 
-// The offsets in LDS, by the whole workgroup.
-__device__ __forceinline__ void mx4_offsets(const Mx4Pass &a, int32_t *o) {
-    for (int i = threadIdx.x; i <= a.n_exp; i += kMx4Threads) o[i] = a.offsets[i];
+// The experts' ends in LDS, by the whole workgroup.
+__device__ __forceinline__ void mx4_ends(const Mx4Pass &a, int32_t *o) {
+    for (int i = threadIdx.x; i < a.n_exp; i += blockDim.x) o[i] = a.offsets[i + 1];
     __syncthreads();
 }
-constexpr int kMx4OffsetBytes = (kMaxExperts + 1 + 63) / 64 * 256;
+constexpr int kMx4EndBytes = kMaxExperts * 4;
 
 // Few rows an expert: bound by the stream of weights.  A wave takes tiles of 64 weight rows and up to 32
 // tokens by itself; weights and tokens pass through a ring of segments in LDS that is the wave's own,
 // filled by direct loads and emptied without a barrier, across the ends of tiles.  SPLIT: too few tiles
 // to occupy the GPU; the four waves of a workgroup then share a tile, each a quarter of the segments,
 // and add up in LDS, which leaves room for two segments a wave instead of three.
-constexpr int kMx4SlotBytes = kMx4WeightBytes + 512 + 32 * 128 + 256;
+constexpr int kMx4SlotBytes = kMx4WeightBytes + 32 * 128;
+constexpr int kMx4ScaleSlot = (64 + 32) * 16;            // of two segments (WIDE); three of 8 bytes a row fit as well
 constexpr int kMx4PartBytes = (kMx4Waves - 1) * 8 * 64 * 16;
 constexpr int mx4_slots(bool split) { return split ? 2 : 3; }
+constexpr int mx4_wave_lds(bool split) { return mx4_slots(split) * kMx4SlotBytes + 2 * kMx4ScaleSlot; }
 constexpr int mx4_stream_lds(bool split) {
-    return kMx4OffsetBytes + kMx4Waves * mx4_slots(split) * kMx4SlotBytes + (split ? kMx4PartBytes : 0);
+    return kMx4EndBytes + kMx4Waves * mx4_wave_lds(split) + (split ? kMx4PartBytes : 0);
 }
 static_assert(mx4_stream_lds(false) <= 160 * 1024 && mx4_stream_lds(true) <= 160 * 1024, "LDS");
 
-template <bool GATEUP, bool SPLIT>
+template <bool GATEUP, bool SPLIT, bool WIDE>
 __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pass a) {
     extern __shared__ __align__(16) char smem[];
     const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, r31 = lane & 31;
-    constexpr int SLOTS = mx4_slots(SPLIT);
-    char *ring = smem + kMx4OffsetBytes + wid * (SLOTS * kMx4SlotBytes);
-    f32x4 *part = (f32x4 *)(smem + kMx4OffsetBytes + kMx4Waves * SLOTS * kMx4SlotBytes);
-    mx4_offsets(a, (int32_t *)smem);
+    constexpr int SLOTS = mx4_slots(SPLIT), SB = mx4_scale_bytes(WIDE);
+    char *ring = smem + kMx4EndBytes + wid * mx4_wave_lds(SPLIT), *scales = ring + SLOTS * kMx4SlotBytes;
+    f32x4 *part = (f32x4 *)(smem + kMx4EndBytes + kMx4Waves * mx4_wave_lds(SPLIT));
+    mx4_ends(a, (int32_t *)smem);
     // gate/up tiles also cover the padding up to whole runs, which is written as zeros
     const int ftiles = GATEUP ? a.hruns * 4 : (a.F + 63) / 64;
     TileList list;
     list.init((const int32_t *)smem, a.n_exp, 32, ftiles, lane);
     const int segs = (a.kruns + 1) / 2;   // with an odd number of runs the last one has no second half
-    const int k0 = SPLIT ? segs * wid / kMx4Waves : 0, k1 = SPLIT ? segs * (wid + 1) / kMx4Waves : segs;
+    // the wave's share of a tile's segments, in pairs where scales come for two
+    constexpr int PAIR = WIDE ? 2 : 1;
+    const int k0 = SPLIT ? segs / PAIR * wid / kMx4Waves * PAIR : 0;
+    const int k1 = SPLIT ? segs / PAIR * (wid + 1) / kMx4Waves * PAIR : segs;
     const int step = SPLIT ? gridDim.x : gridDim.x * kMx4Waves;
     const int first = SPLIT ? blockIdx.x : blockIdx.x * kMx4Waves + wid;
 
     // the tile and segment whose loads are issued next
-    Mx4Weights W;
+    Mx4Weights<WIDE> W;
     const uint8_t *xp[4], *xsp;
-    int it = first, ik = k0, nx = 0;
+    int it = first, ik = k0, nx = 0, is = 0;
     auto next_tile = [&]() {
         int e, ft, row0, valid;
         list.find(it, lane, e, ft, row0, valid);
-        W.aim<GATEUP>(a, e, ft, lane);
+        W.template aim<GATEUP>(a, e, ft, lane);
         // token rows past the tile's repeat its last one; their results are not used
         auto token = [&](int r) {
             const int64_t R = row0 + min(r, valid - 1);
@@ -415,25 +439,34 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
         };
 #pragma unroll
         for (int j = 0; j < 4; ++j) xp[j] = a.x + token(j * 8 + (lane >> 3)) * ((int64_t)a.kruns * 64);
-        xsp = a.xs + token(lane >> 1) * ((int64_t)a.kruns * 4);
+        xsp = a.xs + token(WIDE ? lane & 31 : lane >> 1) * ((int64_t)a.kruns * 4) + (WIDE ? 0 : (lane & 1) * 4);
         nx = (valid + 7) >> 3;
     };
+    // slots of scales: one for each segment, in turn, or one for two
+    auto scale_slot = [&](int s) { return scales + s * (96 * SB); };
+    auto after = [&](int s) { return s + 1 == (WIDE ? 2 : SLOTS) ? 0 : s + 1; };
     // issues the next segment into a slot; the number of loads
     auto issue = [&](int slot) {
         if (it >= list.total || k0 >= k1) return 0;
         if (ik == k0) next_tile();
-        char *dst = ring + slot * kMx4SlotBytes;
-        W.load(a, ik, dst, lane);
+        char *dst = ring + slot * kMx4SlotBytes, *xd = dst + kMx4WeightBytes;
         const bool tail = 2 * ik + 1 == a.kruns;
-        char *xd = dst + kMx4WeightBytes + 512;
+        int n = 8 + nx;
+        if (!WIDE || !(ik & 1)) {
+            char *sd = scale_slot(is);
+            is = after(is);
+            W.load_scales(a, ik, sd, lane);
+            if (!WIDE) dma4(xsp + (int64_t)ik * 8 - (tail && (lane & 1) ? 4 : 0), sd + 64 * SB);
+            else if (lane < 32) dma16(xsp + (int64_t)ik * 8, sd + 64 * SB);
+            n += 3;
+        }
+        W.load(a, ik, dst, lane);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             // the half that an odd number of runs lacks meets weights of zero: it repeats the other
             const int p = (lane & 7) ^ mx4_swz(j * 8 + (lane >> 3));
             if (j < nx) dma16(xp[j] + (int64_t)ik * 128 + (tail ? p & 3 : p) * 16, xd + j * 1024);
         }
-        dma4(xsp + (int64_t)ik * 8 + (tail ? 0 : (lane & 1) * 4), xd + 4096);
-        const int n = kMx4WeightLoads + nx + 1;
         if (++ik == k1) {
             ik = k0;
             it += step;
@@ -445,25 +478,25 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
     issue(0);
     if (SLOTS > 2) n1 = issue(1);
     n2 = issue(SLOTS - 1);
-    int slot = 0;
+    int slot = 0, ss = 0;
     for (int t = first; t < list.total; t += step) {
         f32x16 acc[2] = {};
         for (int k = k0; k < k1; ++k) {
             // the segment's own loads are done once only the later segments' are outstanding
             wait_vmcnt_dyn(n1 + n2);
             asm volatile("" ::: "memory");
-            const char *src = ring + slot * kMx4SlotBytes;
-            const char *xs0 = src + kMx4WeightBytes + 512;
+            const char *src = ring + slot * kMx4SlotBytes, *xsrc = src + kMx4WeightBytes;
+            const char *sc = scale_slot(ss) + (WIDE && (k & 1) ? 8 : 0) + half * 4;
+            if (!WIDE || (k & 1)) ss = after(ss);
             i32x4 w[2][4], x[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 w[0][c] = *(const i32x4 *)(src + mx4_lds(r31, half * 4 + c));
                 w[1][c] = *(const i32x4 *)(src + 4096 + mx4_lds(r31, half * 4 + c));
-                x[c] = *(const i32x4 *)(xs0 + mx4_lds(r31, half * 4 + c));
+                x[c] = *(const i32x4 *)(xsrc + mx4_lds(r31, half * 4 + c));
             }
-            const uint32_t ws0 = *(const uint32_t *)(src + kMx4WeightBytes + (r31 * 2 + half) * 4);
-            const uint32_t ws1 = *(const uint32_t *)(src + kMx4WeightBytes + 256 + (r31 * 2 + half) * 4);
-            const uint32_t xs = *(const uint32_t *)(xs0 + 4096 + (r31 * 2 + half) * 4);
+            const uint32_t ws0 = *(const uint32_t *)(sc + r31 * SB), ws1 = *(const uint32_t *)(sc + (32 + r31) * SB);
+            const uint32_t xs = *(const uint32_t *)(sc + (64 + r31) * SB);
             wait_lgkm0();                  // the slot has been read: it can be filled again
             asm volatile("" ::: "memory");
             const int n = issue(slot);
@@ -509,128 +542,188 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
     }
 }
 
-// Many rows an expert.  A workgroup's tile is 256 weight rows (64 a wave) against up to 256 tokens, one
-// workgroup a compute unit, so that a wave has the registers for 64 x 256 sums.  Segments pass through a
-// ring of stages in LDS, each wave's weight rows for itself and the tokens for all; the fewer token
-// blocks a tile has, the more stages fit.
-constexpr int kMx4TileTokens = 256;
-constexpr int kMx4TileRing = 160 * 1024 - kMx4OffsetBytes;
-// a stage: four waves' weights, then the tokens' codes and scales
-constexpr int mx4_stage_bytes(int tb) { return kMx4Waves * (kMx4WeightBytes + 512) + tb * (32 * 128 + 256); }
+// Many rows an expert.  A workgroup's tile is 256 weight rows against up to 128 tokens.  Four waves, one a SIMD,
+// multiply (64 weight rows each, all tokens); four others, one a SIMD too, only bring segments into a ring of
+// three stages in LDS, across the ends of tiles, so that no product waits behind a load that finds the
+// memory pipeline full.  One barrier a segment: passing it, a segment's loads are done and the stage of the segment
+// before has been read.
+constexpr int kMx4TileThreads = 512;
+constexpr int kMx4TileTokens = 128;
+constexpr int kMx4Stages = 3;
+constexpr int kMx4Stage = 4 * kMx4WeightBytes + kMx4TileTokens * 128;
+// a slot of scales holds 16 bytes a row, of two segments (WIDE), of two slots; three of 8 bytes a row fit as well
+constexpr int kMx4TileRows = 256 + kMx4TileTokens;
+constexpr int kMx4TileLds = kMx4EndBytes + kMx4Stages * kMx4Stage + 2 * kMx4TileRows * 16;
+static_assert(kMx4TileLds <= 160 * 1024, "LDS");
 
-template <bool GATEUP>
-__global__ __launch_bounds__(kMx4Threads, 1) void mx4_tile_kernel(const Mx4Pass a) {
+// The loading waves; wave p brings weight rows 64 p + 0..63, token rows 8 (4 j + p) + 0..7 and the scales of token
+// rows 32 p + 0..31.
+template <bool GATEUP, bool WIDE>
+__device__ __forceinline__ void mx4_tile_load(const Mx4Pass &a, const TileList &list, char *ring, int first, int end,
+                                              int step, int segs, int p, int lane) {
+    constexpr int SB = mx4_scale_bytes(WIDE);
+    char *scales = ring + kMx4Stages * kMx4Stage;
+    Mx4Weights<WIDE> W;
+    const uint8_t *xp[4], *xsp;
+    int t = first, k = 0, tb = 0, is = 0;
+    // issues the next segment into a stage; the number of loads
+    auto issue = [&](char *st) {
+        if (t >= end) return 0;
+        if (k == 0) {
+            int e, ft, row0, valid;
+            list.find(t, lane, e, ft, row0, valid);
+            W.template aim<GATEUP>(a, e, ft * 4 + p, lane);
+            // token row r of the tile; rows past the tile's repeat its last one, their results are not used
+            auto token = [&](int r) {
+                const int64_t R = row0 + min(r, valid - 1);
+                return a.gather ? (int64_t)a.gather[R] : R;
+            };
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xp[j] = a.x + token((j * 4 + p) * 8 + (lane >> 3)) * ((int64_t)a.kruns * 64);
+            xsp = a.xs + token(p * 32 + (WIDE ? lane & 31 : lane >> 1)) * ((int64_t)a.kruns * 4) +
+                  (WIDE ? 0 : (lane & 1) * 4);
+            tb = (valid + 31) >> 5;
+        }
+        const bool tail = 2 * k + 1 == a.kruns;
+        int n = 8 + tb;
+        if (!WIDE || !(k & 1)) {
+            char *sd = scales + is * (kMx4TileRows * SB);
+            is = is + 1 == (WIDE ? 2 : kMx4Stages) ? 0 : is + 1;
+            W.load_scales(a, k, sd + p * (64 * SB), lane);
+            n += 2;
+            if (p < tb) {
+                char *xd = sd + (256 + p * 32) * SB;
+                if (!WIDE) dma4(xsp + (int64_t)k * 8 - (tail && (lane & 1) ? 4 : 0), xd);
+                else if (lane < 32) dma16(xsp + (int64_t)k * 8, xd);
+                ++n;
+            }
+        }
+        W.load(a, k, st + p * kMx4WeightBytes, lane);
+        char *xd = st + 4 * kMx4WeightBytes;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // the half that an odd number of runs lacks meets weights of zero: it repeats the other
+            const int c = (lane & 7) ^ mx4_swz((j * 4 + p) * 8 + (lane >> 3));
+            if (j < tb) dma16(xp[j] + (int64_t)k * 128 + (tail ? c & 3 : c) * 16, xd + (j * 4 + p) * 1024);
+        }
+        if (++k == segs) {
+            k = 0;
+            t += step;
+        }
+        return n;
+    };
+    static_assert(kMx4Stages == 3, "one later segment's loads are under way at a barrier");
+    issue(ring);
+    int later = issue(ring + kMx4Stage);
+    int slot = 2;
+    for (int u = first; u < end; u += step)
+        for (int i = 0; i < segs; ++i) {
+            wait_vmcnt_dyn(later);
+            cta_barrier();
+            later = issue(ring + slot * kMx4Stage);
+            slot = slot == kMx4Stages - 1 ? 0 : slot + 1;
+        }
+    cta_barrier();   // the multiplying waves pass one behind every segment
+}
+
+template <bool GATEUP, bool WIDE>
+__global__ __launch_bounds__(kMx4TileThreads, 1) void mx4_tile_kernel(const Mx4Pass a) {
     extern __shared__ __align__(16) char smem[];
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int half = lane >> 5, r31 = lane & 31;
-    char *ring = smem + kMx4OffsetBytes;
-    mx4_offsets(a, (int32_t *)smem);
+    char *ring = smem + kMx4EndBytes;
+    mx4_ends(a, (int32_t *)smem);
     const int wtiles = GATEUP ? a.hruns * 4 : (a.F + 63) / 64;
-    const int ftiles = (wtiles + kMx4Waves - 1) / kMx4Waves;
     TileList list;
-    list.init((const int32_t *)smem, a.n_exp, kMx4TileTokens, ftiles, lane);
+    list.init((const int32_t *)smem, a.n_exp, kMx4TileTokens, (wtiles + 3) / 4, lane);
     const int segs = (a.kruns + 1) / 2;   // with an odd number of runs the last one has no second half
     // workgroup b runs on XCD b mod 8: each XCD takes a contiguous eighth of the list, so that the row
     // blocks of a weight tile and the weight tiles of a row block meet in its L2
     const int per = (list.total + 7) / 8, xcd = blockIdx.x & 7;
-    const int end = min(list.total, (xcd + 1) * per);
+    const int end = min(list.total, (xcd + 1) * per), first = xcd * per + (blockIdx.x >> 3), step = gridDim.x >> 3;
+    if (first >= end) return;
+    if (wid >= 4) {
+        mx4_tile_load<GATEUP, WIDE>(a, list, ring, first, end, step, segs, wid - 4, lane);
+        return;
+    }
 
-    for (int t = xcd * per + (blockIdx.x >> 3); t < end; t += gridDim.x >> 3) {
-        int e, ft, row0, valid;
-        list.find(t, lane, e, ft, row0, valid);
-        const int wt = ft * kMx4Waves + wid;
-        Mx4Weights W;
-        W.aim<GATEUP>(a, e, wt, lane);
-        // token row r of the tile; rows past the tile's repeat its last one, their results are not used
-        auto token = [&](int r) {
-            const int64_t R = row0 + min(r, valid - 1);
-            return a.gather ? (int64_t)a.gather[R] : R;
+    const int half = lane >> 5, r31 = lane & 31;
+    constexpr int SB = mx4_scale_bytes(WIDE);
+    const char *scales = ring + kMx4Stages * kMx4Stage;
+    int slot = 0, ss = 0, odd = 0, t = first;
+    cta_barrier();                        // the first segment is there
+    auto tile = [&](auto tbc, int ft, int row0, int valid) {
+        constexpr int TB = decltype(tbc)::value;
+        f32x16 acc[2][TB] = {};
+        i32x4 w[2][2], b[2][TB];
+        uint32_t us[2], vs[TB];
+        auto read = [&](int g, int c) {
+            const char *ws = ring + slot * kMx4Stage + wid * kMx4WeightBytes;
+            const char *xb = ring + slot * kMx4Stage + 4 * kMx4WeightBytes;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) w[g][i] = *(const i32x4 *)(ws + i * 4096 + mx4_lds(r31, half * 4 + c));
+#pragma unroll
+            for (int j = 0; j < TB; ++j) b[g][j] = *(const i32x4 *)(xb + mx4_lds(j * 32 + r31, half * 4 + c));
         };
-        auto tile = [&](auto tbc) {
-            constexpr int TB = decltype(tbc)::value;
-            constexpr int STAGE = mx4_stage_bytes(TB), S = kMx4TileRing / STAGE < 4 ? kMx4TileRing / STAGE : 4;
-            constexpr int XO = kMx4Waves * (kMx4WeightBytes + 512);     // tokens within a stage
-            constexpr int XS = (TB + kMx4Waves - 1) / kMx4Waves;        // 256-byte loads of token scales a wave
-            constexpr int N = kMx4WeightLoads + TB + XS;                // loads a wave and segment
-            static_assert(S >= 2 && N * (S - 2) < 64, "ring");
-            // the wave brings token rows 8 (4 j + wid) + 0..7, j < TB, and the scales of rows 32 (4 j + wid) + 0..31
-            // (past the last block those of the last again)
-            const uint8_t *xp[TB], *xsp[XS];
+        auto read_scales = [&]() {
+            const char *sc = scales + ss * (kMx4TileRows * SB) + (WIDE ? odd * 8 : 0) + half * 4;
 #pragma unroll
-            for (int j = 0; j < TB; ++j)
-                xp[j] = a.x + token((j * 4 + wid) * 8 + (lane >> 3)) * ((int64_t)a.kruns * 64);
+            for (int i = 0; i < 2; ++i) us[i] = *(const uint32_t *)(sc + (wid * 64 + i * 32 + r31) * SB);
 #pragma unroll
-            for (int j = 0; j < XS; ++j)
-                xsp[j] = a.xs + token(min(j * 4 + wid, TB - 1) * 32 + (lane >> 1)) * ((int64_t)a.kruns * 4);
-            auto issue = [&](int k, char *st) {
-                W.load(a, k, st + wid * (kMx4WeightBytes + 512), lane);
-                const bool tail = 2 * k + 1 == a.kruns;
-                char *xd = st + XO;
+            for (int j = 0; j < TB; ++j) vs[j] = *(const uint32_t *)(sc + (256 + j * 32 + r31) * SB);
+        };
+        auto next_scales = [&]() {
+            if (!WIDE || odd) ss = ss + 1 == (WIDE ? 2 : kMx4Stages) ? 0 : ss + 1;
+            odd ^= 1;
+            read_scales();
+        };
+        read_scales();
+        read(0, 0);
+        for (int k = 0; k < segs; ++k) {
+            const uint32_t u0 = us[0], u1 = us[1];
+            uint32_t v[TB];
+#pragma unroll
+            for (int j = 0; j < TB; ++j) v[j] = vs[j];
+            auto multiply = [&](auto sc) {
+                constexpr int C = decltype(sc)::value;
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int j = 0; j < TB; ++j) {
-                    // the half that an odd number of runs lacks meets weights of zero: it repeats the other
-                    const int p = (lane & 7) ^ mx4_swz((j * 4 + wid) * 8 + (lane >> 3));
-                    dma16(xp[j] + (int64_t)k * 128 + (tail ? p & 3 : p) * 16, xd + (j * 4 + wid) * 1024);
+                    acc[0][j] = mx4_mfma<C>(w[C & 1][0], b[C & 1][j], acc[0][j], u0, v[j]);
+                    acc[1][j] = mx4_mfma<C>(w[C & 1][1], b[C & 1][j], acc[1][j], u1, v[j]);
+                    mx4_pin(acc[0][j]);
+                    mx4_pin(acc[1][j]);
                 }
-#pragma unroll
-                for (int j = 0; j < XS; ++j)
-                    dma4(xsp[j] + (int64_t)k * 8 + (tail ? 0 : (lane & 1) * 4),
-                         xd + TB * 4096 + min(j * 4 + wid, TB - 1) * 256);
+                __builtin_amdgcn_sched_barrier(0);
             };
-            f32x16 acc[2][TB] = {};
-            cta_barrier();   // every wave is done with the ring
-            for (int k = 0; k < S - 1 && k < segs; ++k) issue(k, ring + k * STAGE);
-            int slot = 0;
-            for (int k = 0; k < segs; ++k) {
-                // the wave's own loads of segment k are done; after the barrier everyone's are, and everyone has
-                // read segment k - 1, whose stage takes segment k + S - 1
-                if (k + S - 1 <= segs) wait_vmcnt<N * (S - 2)>();
-                else wait_vmcnt<0>();
-                cta_barrier();
-                const char *st = ring + slot * STAGE;
-                if (k + S - 1 < segs) issue(k + S - 1, ring + (slot == 0 ? S - 1 : slot - 1) * STAGE);
-                const char *ws = st + wid * (kMx4WeightBytes + 512), *xb = st + XO;
-                uint32_t us[2], vs[TB];
+            read(1, 1);
+            multiply(std::integral_constant<int, 0>{});
+            read(0, 2);
+            multiply(std::integral_constant<int, 1>{});
+            read(1, 3);
+            multiply(std::integral_constant<int, 2>{});
+            // the stage has been read; the next segment's first operands come in behind the last products (after a
+            // tile's last segment they are not used)
+            wait_lgkm0();
+            cta_barrier();
+            slot = slot == kMx4Stages - 1 ? 0 : slot + 1;
+            next_scales();
+            read(0, 0);
+            multiply(std::integral_constant<int, 3>{});
+        }
+        const int wt = ft * 4 + wid;
+        if (wt < wtiles) {
+            const Mx4Out out = mx4_out<GATEUP>(a, row0, valid);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    us[i] = *(const uint32_t *)(ws + kMx4WeightBytes + i * 256 + (r31 * 2 + half) * 4);
-#pragma unroll
-                for (int j = 0; j < TB; ++j) vs[j] = *(const uint32_t *)(xb + TB * 4096 + j * 256 + (r31 * 2 + half) * 4);
-                i32x4 w[2][2], b[2][TB];
-                auto read = [&](int g, int c) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) w[g][i] = *(const i32x4 *)(ws + i * 4096 + mx4_lds(r31, half * 4 + c));
-#pragma unroll
-                    for (int j = 0; j < TB; ++j) b[g][j] = *(const i32x4 *)(xb + mx4_lds(j * 32 + r31, half * 4 + c));
-                };
-                read(0, 0);
-                auto step = [&](auto sc) {
-                    constexpr int C = decltype(sc)::value;
-                    if (C < 3) read((C + 1) & 1, C + 1);
-                    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                    for (int j = 0; j < TB; ++j) {
-                        acc[0][j] = mx4_mfma<C>(w[C & 1][0], b[C & 1][j], acc[0][j], us[0], vs[j]);
-                        acc[1][j] = mx4_mfma<C>(w[C & 1][1], b[C & 1][j], acc[1][j], us[1], vs[j]);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                };
-                step(std::integral_constant<int, 0>{});
-                step(std::integral_constant<int, 1>{});
-                step(std::integral_constant<int, 2>{});
-                step(std::integral_constant<int, 3>{});
-                slot = slot == S - 1 ? 0 : slot + 1;
-            }
-            if (wt < wtiles) {
-                const Mx4Out out = mx4_out<GATEUP>(a, row0, valid);
-#pragma unroll
-                for (int j = 0; j < TB; ++j) mx4_store<GATEUP>(a, out, acc[0][j], acc[1][j], wt, j * 32 + r31, lane);
-            }
-        };
-        if (valid <= 64) tile(std::integral_constant<int, 2>{});
-        else if (valid <= 128) tile(std::integral_constant<int, 4>{});
-        else if (valid <= 192) tile(std::integral_constant<int, 6>{});
-        else tile(std::integral_constant<int, 8>{});
+            for (int j = 0; j < TB; ++j) mx4_store<GATEUP>(a, out, acc[0][j], acc[1][j], wt, j * 32 + r31, lane);
+        }
+    };
+    for (; t < end; t += step) {
+        int e, ft, row0, valid;
+        list.find(t, lane, e, ft, row0, valid);
+        if (valid <= 32) tile(std::integral_constant<int, 1>{}, ft, row0, valid);
+        else if (valid <= 64) tile(std::integral_constant<int, 2>{}, ft, row0, valid);
+        else if (valid <= 96) tile(std::integral_constant<int, 3>{}, ft, row0, valid);
+        else tile(std::integral_constant<int, 4>{}, ft, row0, valid);
     }
 }
 
@@ -697,24 +790,29 @@ hipError_t launch_mx4_ffn(const Mx4Ffn &a, hipStream_t s) {
     down.yvec = (uintptr_t)a.y % 16 == 0 && a.d % 8 == 0;
     const int64_t cus = device_cus();
     const unsigned grid = (unsigned)((cus + 7) / 8 * 8);
-    auto go = [&](auto kernel, int lds, const Mx4Pass &p) {
+    auto go = [&](auto kernel, int threads, int lds, auto... args) {
         const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
-        kernel<<<grid, kMx4Threads, lds, s>>>(p);
+        kernel<<<grid, threads, lds, s>>>(args...);
         return hipGetLastError();
     };
     // 32 rows an expert fill one token block: up to there a tile is bound by its weights
     const bool few = a.max_rows <= 32 * (int64_t)a.n_exp;
     // with fewer tiles than resident waves, at most, a tile takes four waves
     const int64_t experts = a.max_rows < a.n_exp ? a.max_rows : a.n_exp;
-    auto pass = [&](auto gateup, const Mx4Pass &p, int64_t tiles) {
-        constexpr bool GU = decltype(gateup)::value;
-        if (!few) return go(mx4_tile_kernel<GU>, 160 * 1024, p);
-        if (experts * tiles < 4 * cus) return go(mx4_stream_kernel<GU, true>, mx4_stream_lds(true), p);
-        return go(mx4_stream_kernel<GU, false>, mx4_stream_lds(false), p);
+    auto pass = [&](auto gateup, auto wide, const Mx4Pass &p, int64_t tiles) {
+        constexpr bool GU = decltype(gateup)::value, W = decltype(wide)::value;
+        if (!few) return go(mx4_tile_kernel<GU, W>, kMx4TileThreads, kMx4TileLds, p);
+        if (experts * tiles < 4 * cus) return go(mx4_stream_kernel<GU, true, W>, kMx4Threads, mx4_stream_lds(true), p);
+        return go(mx4_stream_kernel<GU, false, W>, kMx4Threads, mx4_stream_lds(false), p);
     };
-    const hipError_t e = pass(std::true_type{}, up, up.hruns * 4);
-    return e != hipSuccess ? e : pass(std::false_type{}, down, (a.d + 63) / 64);
+    auto either = [&](auto gateup, const Mx4Pass &p, int64_t tiles) {
+        const uintptr_t all = (uintptr_t)p.xs | (uintptr_t)p.s0 | (uintptr_t)p.s1;
+        return p.kruns % 4 == 0 && all % 16 == 0 ? pass(gateup, std::true_type{}, p, tiles)
+                                                 : pass(gateup, std::false_type{}, p, tiles);
+    };
+    const hipError_t e = either(std::true_type{}, up, up.hruns * 4);
+    return e != hipSuccess ? e : either(std::false_type{}, down, (a.d + 63) / 64);
 }
 
 }  // namespace moe
