@@ -1,6 +1,7 @@
 // mx4.hip -- microscaled 4-bit floating point (OCP Microscaling Formats v1.0: E2M1 codes,
 // one E8M0 scale for 32 values): rounding, its inverse, and the SwiGLU experts on MX4
 // weights and activations.
+#include <mutex>
 #include <type_traits>
 
 #include "common.h"
@@ -260,8 +261,10 @@ template <bool WIDE>
 struct Mx4Weights {
     __amdgpu_buffer_rsrc_t w[2], s[2];
     uint32_t wo[8], so[2];
+    bool once;
     template <bool GATEUP>
-    __device__ __forceinline__ void aim(const Mx4Pass &a, int e, int ft, int lane) {
+    __device__ __forceinline__ void aim(const Mx4Pass &a, int e, int ft, bool once_, int lane) {
+        once = once_;
         const uint32_t wrow = (uint32_t)a.kruns * 64, srow = (uint32_t)a.kruns * 4;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -279,14 +282,20 @@ struct Mx4Weights {
             so[i] = row < n ? (uint32_t)row * srow + (WIDE ? 0 : (lane & 1) * 4) : kNoOffset;
         }
     }
-    // codes of segment k
+    // Codes of segment k.  Rows that this tile alone reads (an expert of one row block) are loaded with the
+    // nontemporal policy, so that L2 keeps the tokens: decode batch 999 -> 928 us.
     __device__ __forceinline__ void load(const Mx4Pass &a, int k, char *dst, int lane) const {
         const bool tail = 2 * k + 1 == a.kruns;
+        auto each = [&](auto once) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const bool none = tail && (((lane & 7) ^ mx4_swz((q & 3) * 8 + (lane >> 3))) & 4);
-            buffer_dma16(w[q >> 2], none ? kNoOffset : wo[q], k * 128, dst + q * 1024);
-        }
+            for (int q = 0; q < 8; ++q) {
+                const bool none = tail && (((lane & 7) ^ mx4_swz((q & 3) * 8 + (lane >> 3))) & 4);
+                if (decltype(once)::value) buffer_dma16_stream(w[q >> 2], none ? kNoOffset : wo[q], k * 128, dst + q * 1024);
+                else buffer_dma16(w[q >> 2], none ? kNoOffset : wo[q], k * 128, dst + q * 1024);
+            }
+        };
+        if (once) each(std::true_type{});
+        else each(std::false_type{});
     }
     // scales of segment k, or (WIDE) of segments k and k + 1; two loads
     __device__ __forceinline__ void load_scales(const Mx4Pass &a, int k, char *dst, int lane) const {
@@ -431,7 +440,7 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
     auto next_tile = [&]() {
         int e, ft, row0, valid;
         list.find(it, lane, e, ft, row0, valid);
-        W.template aim<GATEUP>(a, e, ft, lane);
+        W.template aim<GATEUP>(a, e, ft, list.blocks(e) == 1, lane);
         // token rows past the tile's repeat its last one; their results are not used
         auto token = [&](int r) {
             const int64_t R = row0 + min(r, valid - 1);
@@ -542,99 +551,144 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
     }
 }
 
-// Many rows an expert.  A workgroup's tile is 256 weight rows against up to 128 tokens.  Four waves, one a SIMD,
-// multiply (64 weight rows each, all tokens); four others, one a SIMD too, only bring segments into a ring of
-// three stages in LDS, across the ends of tiles, so that no product waits behind a load that finds the
-// memory pipeline full.  One barrier a segment: passing it, a segment's loads are done and the stage of the segment
-// before has been read.
+// Many rows an expert.  A workgroup's tile is 256 weight rows against up to CAP blocks of 32 tokens.  Four waves, one a
+// SIMD, multiply (64 weight rows each, all tokens); four others, one a SIMD too, only bring segments into rings in
+// LDS, across the ends of tiles, so that no product waits behind a load that finds the memory pipeline full.  One
+// barrier a segment: passing it, a segment's loads are done and the places of the segment before have been read.
+// CAP 4 leaves room for three segments of weights and of tokens.  CAP 5 leaves room for two of tokens, which come from L2
+// and arrive in time beside weights from memory; it is for experts of about 128 rows, most of which then need
+// one tile and read their weights once.
 constexpr int kMx4TileThreads = 512;
-constexpr int kMx4TileTokens = 128;
-constexpr int kMx4Stages = 3;
-constexpr int kMx4Stage = 4 * kMx4WeightBytes + kMx4TileTokens * 128;
+constexpr int kMx4WeightStages = 3;
+constexpr int mx4_token_stages(int cap) { return cap <= 4 ? 3 : 2; }
 // a slot of scales holds 16 bytes a row, of two segments (WIDE), of two slots; three of 8 bytes a row fit as well
-constexpr int kMx4TileRows = 256 + kMx4TileTokens;
-constexpr int kMx4TileLds = kMx4EndBytes + kMx4Stages * kMx4Stage + 2 * kMx4TileRows * 16;
-static_assert(kMx4TileLds <= 160 * 1024, "LDS");
+constexpr int mx4_tile_lds(int cap) {
+    return kMx4EndBytes + kMx4WeightStages * 4 * kMx4WeightBytes + mx4_token_stages(cap) * cap * 4096 +
+           2 * (256 + cap * 32) * 16;
+}
+static_assert(mx4_tile_lds(4) <= 160 * 1024 && mx4_tile_lds(5) <= 160 * 1024, "LDS");
+// the parts of LDS behind the experts' ends: weights, tokens, scales of weights, scales of tokens
+template <int CAP>
+struct Mx4TileParts {
+    char *w, *x, *ws, *xs;
+    __device__ explicit Mx4TileParts(char *smem) {
+        w = smem + kMx4EndBytes;
+        x = w + kMx4WeightStages * 4 * kMx4WeightBytes;
+        ws = x + mx4_token_stages(CAP) * CAP * 4096;
+        xs = ws + 2 * 256 * 16;
+    }
+};
 
 // The loading waves; wave p brings weight rows 64 p + 0..63, token rows 8 (4 j + p) + 0..7 and the scales of token
-// rows 32 p + 0..31.
-template <bool GATEUP, bool WIDE>
-__device__ __forceinline__ void mx4_tile_load(const Mx4Pass &a, const TileList &list, char *ring, int first, int end,
-                                              int step, int segs, int p, int lane) {
-    constexpr int SB = mx4_scale_bytes(WIDE);
-    char *scales = ring + kMx4Stages * kMx4Stage;
+// rows 32 p + 0..31 (wave 0 also of 128 + 0..31).
+template <bool GATEUP, bool WIDE, int CAP>
+__device__ __forceinline__ void mx4_tile_load(const Mx4Pass &a, const TileList &list, const Mx4TileParts<CAP> &lds,
+                                              int first, int end, int step, int segs, int p, int lane) {
+    constexpr int SB = mx4_scale_bytes(WIDE), XSTAGES = mx4_token_stages(CAP), SSLOTS = WIDE ? 2 : 3;
+    // weights: the tile and segment that come next; places are taken in turn
     Mx4Weights<WIDE> W;
-    const uint8_t *xp[4], *xsp;
-    int t = first, k = 0, tb = 0, is = 0;
-    // issues the next segment into a stage; the number of loads
-    auto issue = [&](char *st) {
-        if (t >= end) return 0;
-        if (k == 0) {
+    int wt = first, wk = 0, wplace = 0, wsplace = 0;
+    auto weights = [&]() {
+        if (wt >= end) return 0;
+        if (wk == 0) {
             int e, ft, row0, valid;
-            list.find(t, lane, e, ft, row0, valid);
-            W.template aim<GATEUP>(a, e, ft * 4 + p, lane);
+            list.find(wt, lane, e, ft, row0, valid);
+            W.template aim<GATEUP>(a, e, ft * 4 + p, list.blocks(e) == 1, lane);
+        }
+        int n = 8;
+        if (!WIDE || !(wk & 1)) {
+            W.load_scales(a, wk, lds.ws + wsplace * (256 * SB) + p * (64 * SB), lane);
+            wsplace = wsplace + 1 == SSLOTS ? 0 : wsplace + 1;
+            n += 2;
+        }
+        W.load(a, wk, lds.w + (wplace * 4 + p) * kMx4WeightBytes, lane);
+        wplace = wplace + 1 == kMx4WeightStages ? 0 : wplace + 1;
+        if (++wk == segs) {
+            wk = 0;
+            wt += step;
+        }
+        return n;
+    };
+    // tokens
+    const uint8_t *xp[CAP], *xsp[2];
+    int xt = first, xk = 0, xplace = 0, xsplace = 0, tb = 0;
+    auto tokens = [&]() {
+        if (xt >= end) return 0;
+        if (xk == 0) {
+            int e, ft, row0, valid;
+            list.find(xt, lane, e, ft, row0, valid);
             // token row r of the tile; rows past the tile's repeat its last one, their results are not used
             auto token = [&](int r) {
                 const int64_t R = row0 + min(r, valid - 1);
                 return a.gather ? (int64_t)a.gather[R] : R;
             };
 #pragma unroll
-            for (int j = 0; j < 4; ++j) xp[j] = a.x + token((j * 4 + p) * 8 + (lane >> 3)) * ((int64_t)a.kruns * 64);
-            xsp = a.xs + token(p * 32 + (WIDE ? lane & 31 : lane >> 1)) * ((int64_t)a.kruns * 4) +
-                  (WIDE ? 0 : (lane & 1) * 4);
+            for (int j = 0; j < CAP; ++j) xp[j] = a.x + token((j * 4 + p) * 8 + (lane >> 3)) * ((int64_t)a.kruns * 64);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                xsp[j] = a.xs + token((j * 4 + p) * 32 + (WIDE ? lane & 31 : lane >> 1)) * ((int64_t)a.kruns * 4) +
+                         (WIDE ? 0 : (lane & 1) * 4);
             tb = (valid + 31) >> 5;
         }
-        const bool tail = 2 * k + 1 == a.kruns;
-        int n = 8 + tb;
-        if (!WIDE || !(k & 1)) {
-            char *sd = scales + is * (kMx4TileRows * SB);
-            is = is + 1 == (WIDE ? 2 : kMx4Stages) ? 0 : is + 1;
-            W.load_scales(a, k, sd + p * (64 * SB), lane);
-            n += 2;
-            if (p < tb) {
-                char *xd = sd + (256 + p * 32) * SB;
-                if (!WIDE) dma4(xsp + (int64_t)k * 8 - (tail && (lane & 1) ? 4 : 0), xd);
-                else if (lane < 32) dma16(xsp + (int64_t)k * 8, xd);
-                ++n;
-            }
-        }
-        W.load(a, k, st + p * kMx4WeightBytes, lane);
-        char *xd = st + 4 * kMx4WeightBytes;
+        const bool tail = 2 * xk + 1 == a.kruns;
+        int n = tb;
+        if (!WIDE || !(xk & 1)) {
+            char *sd = lds.xs + xsplace * (CAP * 32 * SB);
+            xsplace = xsplace + 1 == SSLOTS ? 0 : xsplace + 1;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < (CAP > 4 ? 2 : 1); ++j)
+                if (j * 4 + p < tb) {
+                    char *d = sd + (j * 4 + p) * (32 * SB);
+                    if (!WIDE) dma4(xsp[j] + (int64_t)xk * 8 - (tail && (lane & 1) ? 4 : 0), d);
+                    else if (lane < 32) dma16(xsp[j] + (int64_t)xk * 8, d);
+                    ++n;
+                }
+        }
+        char *xd = lds.x + xplace * (CAP * 4096);
+        xplace = xplace + 1 == XSTAGES ? 0 : xplace + 1;
+#pragma unroll
+        for (int j = 0; j < CAP; ++j) {
             // the half that an odd number of runs lacks meets weights of zero: it repeats the other
             const int c = (lane & 7) ^ mx4_swz((j * 4 + p) * 8 + (lane >> 3));
-            if (j < tb) dma16(xp[j] + (int64_t)k * 128 + (tail ? c & 3 : c) * 16, xd + (j * 4 + p) * 1024);
+            if (j < tb) dma16(xp[j] + (int64_t)xk * 128 + (tail ? c & 3 : c) * 16, xd + (j * 4 + p) * 1024);
         }
-        if (++k == segs) {
-            k = 0;
-            t += step;
+        if (++xk == segs) {
+            xk = 0;
+            xt += step;
         }
         return n;
     };
-    static_assert(kMx4Stages == 3, "one later segment's loads are under way at a barrier");
-    issue(ring);
-    int later = issue(ring + kMx4Stage);
-    int slot = 2;
+    static_assert(kMx4WeightStages == 3 && (XSTAGES == 2 || XSTAGES == 3), "order of the loads");
+    // before the barrier of segment i the loads of segment i have to be done: only later ones may be outstanding,
+    // those of the weights of i + 1 and, with three stages of tokens, of its tokens
+    tokens();
+    weights();
+    int later = XSTAGES == 3 ? tokens() : 0;
+    later += weights();
     for (int u = first; u < end; u += step)
         for (int i = 0; i < segs; ++i) {
             wait_vmcnt_dyn(later);
             cta_barrier();
-            later = issue(ring + slot * kMx4Stage);
-            slot = slot == kMx4Stages - 1 ? 0 : slot + 1;
+            if (XSTAGES == 3) {
+                later = weights();
+                later += tokens();
+            } else {
+                tokens();
+                later = weights();
+            }
         }
     cta_barrier();   // the multiplying waves pass one behind every segment
 }
 
-template <bool GATEUP, bool WIDE>
+template <bool GATEUP, bool WIDE, int CAP>
 __global__ __launch_bounds__(kMx4TileThreads, 1) void mx4_tile_kernel(const Mx4Pass a) {
     extern __shared__ __align__(16) char smem[];
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-    char *ring = smem + kMx4EndBytes;
+    const Mx4TileParts<CAP> lds(smem);
     mx4_ends(a, (int32_t *)smem);
     const int wtiles = GATEUP ? a.hruns * 4 : (a.F + 63) / 64;
     TileList list;
-    list.init((const int32_t *)smem, a.n_exp, kMx4TileTokens, (wtiles + 3) / 4, lane);
+    list.init((const int32_t *)smem, a.n_exp, CAP * 32, (wtiles + 3) / 4, lane);
     const int segs = (a.kruns + 1) / 2;   // with an odd number of runs the last one has no second half
     // workgroup b runs on XCD b mod 8: each XCD takes a contiguous eighth of the list, so that the row
     // blocks of a weight tile and the weight tiles of a row block meet in its L2
@@ -642,14 +696,13 @@ __global__ __launch_bounds__(kMx4TileThreads, 1) void mx4_tile_kernel(const Mx4P
     const int end = min(list.total, (xcd + 1) * per), first = xcd * per + (blockIdx.x >> 3), step = gridDim.x >> 3;
     if (first >= end) return;
     if (wid >= 4) {
-        mx4_tile_load<GATEUP, WIDE>(a, list, ring, first, end, step, segs, wid - 4, lane);
+        mx4_tile_load<GATEUP, WIDE, CAP>(a, list, lds, first, end, step, segs, wid - 4, lane);
         return;
     }
 
     const int half = lane >> 5, r31 = lane & 31;
-    constexpr int SB = mx4_scale_bytes(WIDE);
-    const char *scales = ring + kMx4Stages * kMx4Stage;
-    int slot = 0, ss = 0, odd = 0, t = first;
+    constexpr int SB = mx4_scale_bytes(WIDE), XSTAGES = mx4_token_stages(CAP);
+    int slot = 0, xslot = 0, ss = 0, odd = 0, t = first;
     cta_barrier();                        // the first segment is there
     auto tile = [&](auto tbc, int ft, int row0, int valid) {
         constexpr int TB = decltype(tbc)::value;
@@ -657,22 +710,22 @@ __global__ __launch_bounds__(kMx4TileThreads, 1) void mx4_tile_kernel(const Mx4P
         i32x4 w[2][2], b[2][TB];
         uint32_t us[2], vs[TB];
         auto read = [&](int g, int c) {
-            const char *ws = ring + slot * kMx4Stage + wid * kMx4WeightBytes;
-            const char *xb = ring + slot * kMx4Stage + 4 * kMx4WeightBytes;
+            const char *ws = lds.w + (slot * 4 + wid) * kMx4WeightBytes, *xb = lds.x + xslot * (CAP * 4096);
 #pragma unroll
             for (int i = 0; i < 2; ++i) w[g][i] = *(const i32x4 *)(ws + i * 4096 + mx4_lds(r31, half * 4 + c));
 #pragma unroll
             for (int j = 0; j < TB; ++j) b[g][j] = *(const i32x4 *)(xb + mx4_lds(j * 32 + r31, half * 4 + c));
         };
         auto read_scales = [&]() {
-            const char *sc = scales + ss * (kMx4TileRows * SB) + (WIDE ? odd * 8 : 0) + half * 4;
+            const int at = (WIDE ? odd * 8 : 0) + half * 4;
+            const char *ws = lds.ws + ss * (256 * SB) + at, *xs = lds.xs + ss * (CAP * 32 * SB) + at;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) us[i] = *(const uint32_t *)(sc + (wid * 64 + i * 32 + r31) * SB);
+            for (int i = 0; i < 2; ++i) us[i] = *(const uint32_t *)(ws + (wid * 64 + i * 32 + r31) * SB);
 #pragma unroll
-            for (int j = 0; j < TB; ++j) vs[j] = *(const uint32_t *)(sc + (256 + j * 32 + r31) * SB);
+            for (int j = 0; j < TB; ++j) vs[j] = *(const uint32_t *)(xs + (j * 32 + r31) * SB);
         };
         auto next_scales = [&]() {
-            if (!WIDE || odd) ss = ss + 1 == (WIDE ? 2 : kMx4Stages) ? 0 : ss + 1;
+            if (!WIDE || odd) ss = ss + 1 == (WIDE ? 2 : 3) ? 0 : ss + 1;
             odd ^= 1;
             read_scales();
         };
@@ -705,7 +758,8 @@ __global__ __launch_bounds__(kMx4TileThreads, 1) void mx4_tile_kernel(const Mx4P
             // tile's last segment they are not used)
             wait_lgkm0();
             cta_barrier();
-            slot = slot == kMx4Stages - 1 ? 0 : slot + 1;
+            slot = slot == kMx4WeightStages - 1 ? 0 : slot + 1;
+            xslot = xslot == XSTAGES - 1 ? 0 : xslot + 1;
             next_scales();
             read(0, 0);
             multiply(std::integral_constant<int, 3>{});
@@ -723,8 +777,21 @@ __global__ __launch_bounds__(kMx4TileThreads, 1) void mx4_tile_kernel(const Mx4P
         if (valid <= 32) tile(std::integral_constant<int, 1>{}, ft, row0, valid);
         else if (valid <= 64) tile(std::integral_constant<int, 2>{}, ft, row0, valid);
         else if (valid <= 96) tile(std::integral_constant<int, 3>{}, ft, row0, valid);
-        else tile(std::integral_constant<int, 4>{}, ft, row0, valid);
+        else if (CAP == 4 || valid <= 128) tile(std::integral_constant<int, 4>{}, ft, row0, valid);
+        else tile(std::integral_constant<int, CAP>{}, ft, row0, valid);
     }
+}
+
+template <void (*KERNEL)(Mx4Pass)>
+hipError_t mx4_launch(unsigned grid, int threads, int lds, const Mx4Pass &p, hipStream_t s) {
+    static std::once_flag once;
+    static hipError_t attr = hipSuccess;
+    std::call_once(once, [&] {
+        attr = hipFuncSetAttribute((const void *)KERNEL, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    });
+    if (attr != hipSuccess) return attr;
+    KERNEL<<<grid, threads, lds, s>>>(p);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -790,21 +857,23 @@ hipError_t launch_mx4_ffn(const Mx4Ffn &a, hipStream_t s) {
     down.yvec = (uintptr_t)a.y % 16 == 0 && a.d % 8 == 0;
     const int64_t cus = device_cus();
     const unsigned grid = (unsigned)((cus + 7) / 8 * 8);
-    auto go = [&](auto kernel, int threads, int lds, auto... args) {
-        const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess) return e;
-        kernel<<<grid, threads, lds, s>>>(args...);
-        return hipGetLastError();
-    };
-    // 32 rows an expert fill one token block: up to there a tile is bound by its weights
-    const bool few = a.max_rows <= 32 * (int64_t)a.n_exp;
-    // with fewer tiles than resident waves, at most, a tile takes four waves
+    // Up to 16 rows an expert on average a tile is bound by its weights, whose stream the per-wave rings keep
+    // up best (256 experts of 7168 x 2048: 917 us at 4 rows, where the tile kernel has half its places empty;
+    // at 20 rows 1118 us against the tile kernel's 1030, at 60 rows 1850 against 1210).
+    const bool few = a.max_rows <= 16 * (int64_t)a.n_exp;
+    // Four waves share a tile where the experts' tiles would not give half the waves one: one token, 8 of
+    // those experts: gate/up (512 tiles) 24 us against 30, down (896 tiles) 20 against 13 without sharing.
     const int64_t experts = a.max_rows < a.n_exp ? a.max_rows : a.n_exp;
+    // One tile instead of two for most experts of 112 to 160 rows: 128 rows on average 1430 us against 1560;
+    // outside, three stages of tokens do better (97 rows of a small, skewed case 22 us against 24).
+    const bool tall = a.max_rows > 112 * (int64_t)a.n_exp && a.max_rows <= 160 * (int64_t)a.n_exp;
     auto pass = [&](auto gateup, auto wide, const Mx4Pass &p, int64_t tiles) {
         constexpr bool GU = decltype(gateup)::value, W = decltype(wide)::value;
-        if (!few) return go(mx4_tile_kernel<GU, W>, kMx4TileThreads, kMx4TileLds, p);
-        if (experts * tiles < 4 * cus) return go(mx4_stream_kernel<GU, true, W>, kMx4Threads, mx4_stream_lds(true), p);
-        return go(mx4_stream_kernel<GU, false, W>, kMx4Threads, mx4_stream_lds(false), p);
+        if (!few && tall) return mx4_launch<mx4_tile_kernel<GU, W, 5>>(grid, kMx4TileThreads, mx4_tile_lds(5), p, s);
+        if (!few) return mx4_launch<mx4_tile_kernel<GU, W, 4>>(grid, kMx4TileThreads, mx4_tile_lds(4), p, s);
+        if (experts * tiles <= 2 * cus)
+            return mx4_launch<mx4_stream_kernel<GU, true, W>>(grid, kMx4Threads, mx4_stream_lds(true), p, s);
+        return mx4_launch<mx4_stream_kernel<GU, false, W>>(grid, kMx4Threads, mx4_stream_lds(false), p, s);
     };
     auto either = [&](auto gateup, const Mx4Pass &p, int64_t tiles) {
         const uintptr_t all = (uintptr_t)p.xs | (uintptr_t)p.s0 | (uintptr_t)p.s1;
