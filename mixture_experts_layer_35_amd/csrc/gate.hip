@@ -58,10 +58,31 @@ __device__ __forceinline__ float lanes_sum(float v) {
         return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
     }));
 }
+// The same steps on both halves of a double.
 template <int L>
 __device__ __forceinline__ double lanes_sum(double v) {
-#pragma unroll
-    for (int m = 1; m < L; m <<= 1) v += __shfl_xor(v, m, 64);
+    auto dpp = [](double x, auto ctrl) {
+        const u32x2 h = __builtin_bit_cast(u32x2, x);
+        const u32x2 o = {(uint32_t)__builtin_amdgcn_update_dpp((int)h[0], (int)h[0], decltype(ctrl)::value, 0xF, 0xF, false),
+                         (uint32_t)__builtin_amdgcn_update_dpp((int)h[1], (int)h[1], decltype(ctrl)::value, 0xF, 0xF, false)};
+        return __builtin_bit_cast(double, o);
+    };
+    v += dpp(v, std::integral_constant<int, 0xB1>{});
+    v += dpp(v, std::integral_constant<int, 0x4E>{});
+    if (L >= 8) v += dpp(v, std::integral_constant<int, 0x141>{});
+    if (L >= 16) v += dpp(v, std::integral_constant<int, 0x140>{});
+    if (L >= 32) {
+        const u32x2 h = __builtin_bit_cast(u32x2, v);
+        const auto lo = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+        v = __builtin_bit_cast(double, u32x2{lo[0], hi[0]}) + __builtin_bit_cast(double, u32x2{lo[1], hi[1]});
+    }
+    if (L >= 64) {
+        const u32x2 h = __builtin_bit_cast(u32x2, v);
+        const auto lo = __builtin_amdgcn_permlane32_swap(h[0], h[0], false, false);
+        const auto hi = __builtin_amdgcn_permlane32_swap(h[1], h[1], false, false);
+        v = __builtin_bit_cast(double, u32x2{lo[0], hi[0]}) + __builtin_bit_cast(double, u32x2{lo[1], hi[1]});
+    }
     return v;
 }
 
@@ -119,48 +140,54 @@ __device__ __forceinline__ float load1(const void *p, int64_t i) {
     return DT == DT_F32 ? ((const float *)p)[i] : bf16_to_f32(((const uint16_t *)p)[i]);
 }
 
-// V values of a row from element i0 on; `fill` past element n.
-template <int DT, int V>
-__device__ __forceinline__ void load_row(const void *row, int i0, int n, bool vec, float fill, float (&v)[V]) {
-    if (vec && i0 + V <= n) {
-        if (DT == DT_F32) {
+// A lane's V values of a row of n, four at a time: chunk r of lane l starts at chunk_at<L, V, SPREAD>(l, r).  In
+// order (a lane's values are neighbours), or spread (the lanes' chunks are, which the memory pipeline likes
+// better).  `fill` past element n.
+template <int L, int V, bool SPREAD>
+__device__ __forceinline__ int chunk_at(int l, int r) { return SPREAD ? (r * L + l) * 4 : l * V + r * 4; }
+
+template <int DT, int L, int V, bool SPREAD>
+__device__ __forceinline__ void load_row(const void *row, int l, int n, bool vec, float fill, float (&v)[V]) {
 #pragma unroll
-            for (int r = 0; r < V; r += 4) {
-                const f32x4 x = *(const f32x4 *)((const float *)row + i0 + r);
+    for (int r = 0; r < V / 4; ++r) {
+        const int i = chunk_at<L, V, SPREAD>(l, r);
+        float *o = v + 4 * r;
+        if (vec && i + 4 <= n) {
+            if (DT == DT_F32) {
+                const f32x4 x = *(const f32x4 *)((const float *)row + i);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[r + k] = x[k];
+                for (int k = 0; k < 4; ++k) o[k] = x[k];
+            } else {
+                const u32x2 x = *(const u32x2 *)((const uint16_t *)row + i);
+                o[0] = __uint_as_float(x[0] << 16);
+                o[1] = __uint_as_float(x[0] & 0xFFFF0000u);
+                o[2] = __uint_as_float(x[1] << 16);
+                o[3] = __uint_as_float(x[1] & 0xFFFF0000u);
             }
         } else {
 #pragma unroll
-            for (int r = 0; r < V; r += 4) {
-                const u32x2 x = *(const u32x2 *)((const uint16_t *)row + i0 + r);
-                v[r] = __uint_as_float(x[0] << 16);
-                v[r + 1] = __uint_as_float(x[0] & 0xFFFF0000u);
-                v[r + 2] = __uint_as_float(x[1] << 16);
-                v[r + 3] = __uint_as_float(x[1] & 0xFFFF0000u);
-            }
+            for (int k = 0; k < 4; ++k) o[k] = i + k < n ? load1<DT>(row, i + k) : fill;
         }
-        return;
     }
-#pragma unroll
-    for (int r = 0; r < V; ++r) v[r] = i0 + r < n ? load1<DT>(row, i0 + r) : fill;
 }
 
-template <int DT, int V>
-__device__ __forceinline__ void store_row(void *row, int i0, int n, bool vec, const float (&v)[V]) {
-    if (vec && i0 + V <= n) {
+template <int DT, int L, int V, bool SPREAD>
+__device__ __forceinline__ void store_row(void *row, int l, int n, bool vec, const float (&v)[V]) {
 #pragma unroll
-        for (int r = 0; r < V; r += 4) {
-            if (DT == DT_F32) *(f32x4 *)((float *)row + i0 + r) = f32x4{v[r], v[r + 1], v[r + 2], v[r + 3]};
-            else *(u32x2 *)((uint16_t *)row + i0 + r) = u32x2{pack_bf16x2(v[r], v[r + 1]), pack_bf16x2(v[r + 2], v[r + 3])};
+    for (int r = 0; r < V / 4; ++r) {
+        const int i = chunk_at<L, V, SPREAD>(l, r);
+        const float *o = v + 4 * r;
+        if (vec && i + 4 <= n) {
+            if (DT == DT_F32) *(f32x4 *)((float *)row + i) = f32x4{o[0], o[1], o[2], o[3]};
+            else *(u32x2 *)((uint16_t *)row + i) = u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (i + k >= n) continue;
+                if (DT == DT_F32) ((float *)row)[i + k] = o[k];
+                else ((uint16_t *)row)[i + k] = (uint16_t)pack_bf16x2(o[k], 0.0f);
+            }
         }
-        return;
-    }
-#pragma unroll
-    for (int r = 0; r < V; ++r) {
-        if (i0 + r >= n) continue;
-        if (DT == DT_F32) ((float *)row)[i0 + r] = v[r];
-        else ((uint16_t *)row)[i0 + r] = (uint16_t)pack_bf16x2(v[r], 0.0f);
     }
 }
 
@@ -191,32 +218,55 @@ __device__ __forceinline__ void softmax_stats(const float (&z)[V], float (&e)[V]
     m = lanes_max<L>(t);
     // the sum is held in 64 bits and rounded once, so that no order of the additions can move a choice
     double sum = 0.0;
+    if (__any(m == -neg_inf())) {
 #pragma unroll
-    for (int r = 0; r < V; ++r) {
-        e[r] = softmax_exp(z[r], m);
-        sum += e[r];
+        for (int r = 0; r < V; ++r) e[r] = softmax_exp(z[r], m);
+    } else {
+        const float base = m == neg_inf() ? 0.0f : m;
+#pragma unroll
+        for (int r = 0; r < V; ++r) e[r] = expf((in_use(z[r]) ? z[r] : neg_inf()) - base);   // softmax_exp's bits
     }
+#pragma unroll
+    for (int r = 0; r < V; ++r) sum += e[r];
     const float total = (float)lanes_sum<L>(sum);
     inv = total > 0.0f ? 1.0f / total : 0.0f;
 }
 
-// LDS of a token: the slots' keys and indices, the scores, and with groups the choice values (a
-// group's a word apart from the next one's bank) and the groups' keys.
-__host__ __device__ inline int gate_lds_words(int E, int G) {
-    return 2 * kMaxK + ((E + 3) & ~3) + (G > 1 ? E + 2 * G : 0) + 1;
+// LDS of a token: the slots' keys and indices, with a bias the scores, and for groups that do not lie in whole
+// lanes the choice values (each group a word apart from the next one's bank) and the groups' keys.
+__host__ __device__ inline int gate_lds_words(int E, int G, bool bias) {
+    return 2 * kMaxK + (bias ? (E + 3) & ~3 : 0) + (G > 1 ? (E + 2 * G + 3) & ~3 : 0);
+}
+
+// The two largest keys of the `width` lanes (a power of two) around a lane, in all of them.
+__device__ __forceinline__ void lanes_top2(uint32_t &k1, uint32_t &k2, int width) {
+    auto join = [&](uint32_t o1, uint32_t o2) {
+        k2 = max(min(k1, o1), max(k2, o2));
+        k1 = max(k1, o1);
+    };
+    auto dpp = [&](auto ctrl) {
+        join((uint32_t)__builtin_amdgcn_update_dpp((int)k1, (int)k1, decltype(ctrl)::value, 0xF, 0xF, false),
+             (uint32_t)__builtin_amdgcn_update_dpp((int)k2, (int)k2, decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    if (width >= 2) dpp(std::integral_constant<int, 0xB1>{});
+    if (width >= 4) dpp(std::integral_constant<int, 0x4E>{});
+    if (width >= 8) dpp(std::integral_constant<int, 0x141>{});
+    if (width >= 16) dpp(std::integral_constant<int, 0x140>{});
+    if (width >= 32) join((uint32_t)__shfl_xor((int)k1, 16, 64), (uint32_t)__shfl_xor((int)k2, 16, 64));
 }
 
 template <int DT, int L, int V>
 __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs a) {
     constexpr int TPB = kGateThreads / L;                 // tokens per workgroup
     constexpr int Q = L < kMaxK ? kMaxK / L : 1;          // slots a lane handles, at most
-    extern __shared__ uint32_t lds[];
+    extern __shared__ __align__(16) uint32_t lds[];
     const int sub = threadIdx.x / L, l = threadIdx.x % L, lane = threadIdx.x & 63, base = lane / L * L;
-    const int E = a.E, K = a.K, G = a.G;
-    uint32_t *slot_key = lds + sub * gate_lds_words(E, G);
+    const int E = a.E, K = a.K, G = a.G, E4 = (E + 3) & ~3;
+    const bool bias = a.bias != nullptr;
+    uint32_t *slot_key = lds + sub * gate_lds_words(E, G, bias);
     int *slot_idx = (int *)(slot_key + kMaxK);
     float *sval = (float *)(slot_idx + kMaxK);
-    uint32_t *ckey = (uint32_t *)(sval + ((E + 3) & ~3));
+    uint32_t *ckey = (uint32_t *)(sval + (bias ? E4 : 0));
     uint32_t *gkey = ckey + E + G;
     // the wave's tokens past T work on the last one and store nothing
     const int64_t t0 = (int64_t)blockIdx.x * TPB + sub;
@@ -226,8 +276,8 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs a) {
     const int i0 = l * V;
 
     float z[V], b[V], s[V];
-    load_row<DT, V>(row, i0, E, a.vec, neg_inf(), z);
-    if (a.bias) load_row<DT_F32, V>(a.bias, i0, E, a.bvec, 0.0f, b);
+    load_row<DT, L, V, false>(row, l, E, a.vec, neg_inf(), z);
+    if (bias) load_row<DT_F32, L, V, false>(a.bias, l, E, a.bvec, 0.0f, b);
     if (a.softmax) {
         float m, inv;
         softmax_stats<L, V>(z, s, m, inv);
@@ -236,67 +286,99 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs a) {
     } else {
         sigmoid_scores<V>(z, s);
     }
+    // an expert out of use, or whose choice value is NaN (which fmaxf passes over), orders as -infinity
     uint32_t key[V];
+    if (bias) {
 #pragma unroll
-    for (int r = 0; r < V; ++r) {
-        const float c = a.bias ? s[r] + b[r] : s[r];
-        // an expert out of use, or whose choice value is NaN, orders as -infinity
-        key[r] = in_use(z[r]) && c == c ? choice_key(c) : kKeyNone;
-        if (i0 + r >= E) key[r] = 0u;
-        if (i0 + r < E) sval[i0 + r] = s[r];
+        for (int r = 0; r < V; ++r) key[r] = choice_key(in_use(z[r]) ? fmaxf(s[r] + b[r], neg_inf()) : neg_inf());
+#pragma unroll
+        for (int r = 0; r < V; r += 4)
+            if (i0 + r < E) *(f32x4 *)(sval + i0 + r) = f32x4{s[r], s[r + 1], s[r + 2], s[r + 3]};
+    } else {
+#pragma unroll
+        for (int r = 0; r < V; ++r) key[r] = in_use(z[r]) ? __float_as_uint(s[r]) | 0x80000000u : kKeyNone;
     }
-    if (a.scores && live) store_row<DT_F32, V>(a.scores + t * E, i0, E, a.svec, s);
+    if (E != L * V) {
+#pragma unroll
+        for (int r = 0; r < V; ++r)
+            if (i0 + r >= E) key[r] = 0u;
+    }
+    if (a.scores && live) store_row<DT_F32, L, V, false>(a.scores + t * E, l, E, a.svec, s);
 
     if (G > 1) {
         const int gs = E / G;
-        int g = i0 / gs, left = (g + 1) * gs - i0;
-#pragma unroll
-        for (int r = 0; r < V; ++r) {
-            if (i0 + r < E) ckey[i0 + r + g] = key[r];
-            if (--left == 0) {
-                ++g;
-                left = gs;
-            }
-        }
-        token_lds_order();
-        // a group's two largest keys, by one lane
-        for (int o = l; o < G; o += L) {
+        auto group_key = [&](uint32_t k1, uint32_t k2) {
+            return !a.group_max && k2 > kKeyNone ? choice_key(key_value(k1) + key_value(k2)) : k1;
+        };
+        if (E == L * V && gs % V == 0 && G <= 16) {
+            // a group is L / G whole lanes: its keys stay in registers
+            const int width = L / G, mine = l / width;
             uint32_t k1 = 0, k2 = 0;
-            const uint32_t *p = ckey + o * (gs + 1);
-#pragma unroll 8
-            for (int i = 0; i < gs; ++i) {
-                const uint32_t c = p[i];
-                k2 = max(k2, min(k1, c));
-                k1 = max(k1, c);
-            }
-            if (!a.group_max && k2 > kKeyNone) k1 = choice_key(key_value(k1) + key_value(k2));
-            gkey[o] = k1;
-        }
-        token_lds_order();
-        // a group is kept when fewer than M others come before it
-        uint32_t lo = 0, hi = 0;
-        for (int o = l; o < G; o += L) {
-            const uint32_t k = gkey[o];
-            int before = 0;
-#pragma unroll 8
-            for (int p = 0; p < G; ++p) before += gkey[p] > k || (gkey[p] == k && p < o) ? 1 : 0;
-            if (before < a.M) {
-                if (o < 32) lo |= 1u << o;
-                else hi |= 1u << (o - 32);
-            }
-        }
-        auto either = [](uint32_t x, uint32_t y) { return x | y; };
-        lo = lanes_reduce<L>(lo, either);
-        if (G > 32) hi = lanes_reduce<L>(hi, either);
-        const uint64_t kept = (uint64_t)hi << 32 | lo;
-        g = i0 / gs;
-        left = (g + 1) * gs - i0;
 #pragma unroll
-        for (int r = 0; r < V; ++r) {
-            if (!((kept >> (g & 63)) & 1)) key[r] = min(key[r], kKeyNone);
-            if (--left == 0) {
-                ++g;
-                left = gs;
+            for (int r = 0; r < V; ++r) {
+                k2 = max(k2, min(k1, key[r]));
+                k1 = max(k1, key[r]);
+            }
+            lanes_top2(k1, k2, width);
+            const uint32_t k = group_key(k1, k2);
+            // kept when fewer than M groups come before it
+            int before = 0;
+            for (int o = 0; o < G; ++o) {
+                const uint32_t other = (uint32_t)__shfl((int)k, base + o * width, 64);
+                before += other > k || (other == k && o < mine) ? 1 : 0;
+            }
+            const uint32_t most = before < a.M ? 0xFFFFFFFFu : kKeyNone;
+#pragma unroll
+            for (int r = 0; r < V; ++r) key[r] = min(key[r], most);
+        } else {
+            int g = i0 / gs, left = (g + 1) * gs - i0;
+#pragma unroll
+            for (int r = 0; r < V; ++r) {
+                if (i0 + r < E) ckey[i0 + r + g] = key[r];
+                if (--left == 0) {
+                    ++g;
+                    left = gs;
+                }
+            }
+            token_lds_order();
+            // a group's two largest keys, by one lane
+            for (int o = l; o < G; o += L) {
+                uint32_t k1 = 0, k2 = 0;
+                const uint32_t *p = ckey + o * (gs + 1);
+#pragma unroll 8
+                for (int i = 0; i < gs; ++i) {
+                    const uint32_t c = p[i];
+                    k2 = max(k2, min(k1, c));
+                    k1 = max(k1, c);
+                }
+                gkey[o] = group_key(k1, k2);
+            }
+            token_lds_order();
+            // a group is kept when fewer than M others come before it
+            uint32_t lo = 0, hi = 0;
+            for (int o = l; o < G; o += L) {
+                const uint32_t k = gkey[o];
+                int before = 0;
+#pragma unroll 8
+                for (int p = 0; p < G; ++p) before += gkey[p] > k || (gkey[p] == k && p < o) ? 1 : 0;
+                if (before < a.M) {
+                    if (o < 32) lo |= 1u << o;
+                    else hi |= 1u << (o - 32);
+                }
+            }
+            auto either = [](uint32_t x, uint32_t y) { return x | y; };
+            lo = lanes_reduce<L>(lo, either);
+            if (G > 32) hi = lanes_reduce<L>(hi, either);
+            const uint64_t kept = (uint64_t)hi << 32 | lo;
+            g = i0 / gs;
+            left = (g + 1) * gs - i0;
+#pragma unroll
+            for (int r = 0; r < V; ++r) {
+                if (!((kept >> (g & 63)) & 1)) key[r] = min(key[r], kKeyNone);
+                if (--left == 0) {
+                    ++g;
+                    left = gs;
+                }
             }
         }
     }
@@ -323,14 +405,15 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs a) {
         }
     }
     token_lds_order();
-    // the slots' weights, and their sum from left to right
+    // the slots' weights (without a bias a key is its score), and their sum from left to right
     float w[Q];
     int ix[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         const int j = min(l + q * L, K - 1);
         ix[q] = slot_idx[j];
-        w[q] = slot_key[j] == kKeyNone ? 0.0f : sval[ix[q]];
+        const uint32_t k = slot_key[j];
+        w[q] = k == kKeyNone ? 0.0f : bias ? sval[ix[q]] : key_value(k);
     }
     if (a.renorm) {
         token_lds_order();
@@ -355,7 +438,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs a) {
     }
 }
 
-__host__ __device__ inline int gate_backward_lds_words(int E) { return ((E + 3) & ~3) + 1; }
+__host__ __device__ inline int gate_backward_lds_words(int E) { return (E + 3) & ~3; }
 
 // DENSE: softmax scores, or a gradient at every score.  Otherwise only the chosen logits have a
 // gradient, and only they are read.
@@ -363,7 +446,7 @@ template <int DT, int L, int V, bool DENSE>
 __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(const GateArgs a) {
     constexpr int TPB = kGateThreads / L;
     constexpr int Q = L < kMaxK ? kMaxK / L : 1;
-    extern __shared__ uint32_t lds[];
+    extern __shared__ __align__(16) uint32_t lds[];
     const int sub = threadIdx.x / L, l = threadIdx.x % L;
     const int E = a.E, K = a.K;
     float *dsl = (float *)(lds + sub * gate_backward_lds_words(E));   // the slots' part of ds, or of dz
@@ -371,7 +454,6 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(const GateA
     const bool live = t0 < a.T;
     const int64_t t = live ? t0 : a.T - 1;
     const char *row = (const char *)a.logits + t * a.ld * (DT == DT_F32 ? 4 : 2);
-    const int i0 = l * V;
 
     float z[V], d[V], m = 0.0f, inv = 0.0f;
     int ij[Q];
@@ -387,15 +469,17 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(const GateA
     }
     const float w0 = a.cw[t * K], dw0 = a.dw[t * K];
     if (DENSE) {
-        load_row<DT, V>(row, i0, E, a.vec, neg_inf(), z);
-        if (a.ds) load_row<DT_F32, V>(a.ds + t * E, i0, E, a.svec, 0.0f, d);
+        load_row<DT, L, V, true>(row, l, E, a.vec, neg_inf(), z);
+        if (a.ds) load_row<DT_F32, L, V, true>(a.ds + t * E, l, E, a.svec, 0.0f, d);
     }
     // the slots' logits; slots without a weight read the first one and do not use it
 #pragma unroll
     for (int q = 0; q < Q; ++q) sj[q] = load1<DT>(row, max(ij[q], 0));
 #pragma unroll
-    for (int r = 0; r < V; ++r)
-        if (i0 + r < E) dsl[i0 + r] = 0.0f;
+    for (int r = 0; r < V / 4; ++r) {
+        const int i = chunk_at<L, V, true>(l, r);
+        if (i < E) *(f32x4 *)(dsl + i) = f32x4{0, 0, 0, 0};
+    }
 
     float s[V];
     if (DENSE) {
@@ -437,7 +521,12 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(const GateA
 
     float o[V];
 #pragma unroll
-    for (int r = 0; r < V; ++r) o[r] = i0 + r < E ? dsl[i0 + r] : 0.0f;
+    for (int r = 0; r < V / 4; ++r) {
+        const int i = chunk_at<L, V, true>(l, r);
+        const f32x4 x = i < E ? *(const f32x4 *)(dsl + i) : f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[4 * r + k] = x[k];
+    }
     if (DENSE) {
         float dot = 0.0f;
 #pragma unroll
@@ -450,7 +539,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(const GateA
 #pragma unroll
         for (int r = 0; r < V; ++r) o[r] = a.softmax ? s[r] * (o[r] - dot) : o[r] * s[r] * (1.0f - s[r]);
     }
-    if (live) store_row<DT, V>((char *)a.dlogits + t * a.dld * (DT == DT_F32 ? 4 : 2), i0, E, a.dvec, o);
+    if (live) store_row<DT, L, V, true>((char *)a.dlogits + t * a.dld * (DT == DT_F32 ? 4 : 2), l, E, a.dvec, o);
 }
 
 // f(L, V) for a token width that holds E experts.  Up to 16 values a lane keep a wave on four tokens
@@ -461,7 +550,10 @@ hipError_t with_width(int64_t T, int E, F f) {
     using std::integral_constant;
     const bool few = T * ((E + 3) / 4) <= (int64_t)device_cus() * 4 * 64;   // lanes of 4 values fill one wave a SIMD
     if (E <= 32) return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
-    if (E <= 64) return f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+    if (E <= 64) {
+        if (few) return f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+        return f(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    }
     if (E <= 128) {
         if (few) return f(integral_constant<int, 32>{}, integral_constant<int, 4>{});
         return f(integral_constant<int, 16>{}, integral_constant<int, 8>{});
@@ -511,7 +603,7 @@ hipError_t launch_gate(const GateProblem &p, const float *bias, float *scores, i
     return with_width(p.T, p.E, [&](auto lc, auto vc) {
         constexpr int L = decltype(lc)::value, V = decltype(vc)::value, TPB = kGateThreads / L;
         const unsigned grid = (unsigned)((p.T + TPB - 1) / TPB);
-        const size_t lds = (size_t)TPB * gate_lds_words(p.E, p.G) * 4;
+        const size_t lds = (size_t)TPB * gate_lds_words(p.E, p.G, bias != nullptr) * 4;
         if (p.dt == DT_F32) gate_kernel<DT_F32, L, V><<<grid, kGateThreads, lds, s>>>(a);
         else gate_kernel<DT_BF16, L, V><<<grid, kGateThreads, lds, s>>>(a);
         return hipGetLastError();
