@@ -38,19 +38,36 @@ __device__ __forceinline__ uint32_t mx4_codes(const float (&v)[8], uint32_t s) {
     return c;
 }
 
+// Row and run of run g of a matrix of rows of `runs` runs.  FLAT: the rows are whole runs without gaps, so the
+// matrix is one row (the division of 64-bit indices took longer than the memory).
+template <bool FLAT>
+__device__ __forceinline__ void mx4_place(int64_t g, int64_t total, int64_t runs, int64_t &r, int64_t &c) {
+    if (FLAT) {
+        r = 0;
+        c = g;
+    } else if (total < (1ll << 31)) {
+        const uint32_t q = (uint32_t)g / (uint32_t)runs;
+        r = q;
+        c = (uint32_t)g - q * (uint32_t)runs;
+    } else {
+        r = g / runs;
+        c = g - r * runs;
+    }
+}
+
 // 16 lanes per run of 128 values, eight values a lane, four lanes a block.
-template <int DT, bool VEC>
+template <int DT, bool VEC, bool FLAT>
 __global__ __launch_bounds__(256) void mx4_quantize_kernel(const void *__restrict__ x, int64_t ld, int64_t rows,
-                                                           int cols, int runs, uint8_t *__restrict__ q,
+                                                           int64_t cols, int64_t runs, uint8_t *__restrict__ q,
                                                            uint8_t *__restrict__ sc) {
     const int64_t total = rows * runs;
     const int sub = threadIdx.x & 15;
     // the loop bound is uniform over the workgroup, so every lane reaches the lane exchanges
     for (int64_t g0 = (int64_t)blockIdx.x * 16; g0 < total; g0 += (int64_t)gridDim.x * 16) {
         const int64_t g = g0 + (threadIdx.x >> 4);
-        const int64_t gg = g < total ? g : total - 1;
-        const int64_t r = gg / runs;
-        const int c0 = (int)(gg - r * runs) * 128 + sub * 8;
+        int64_t r, c;
+        mx4_place<FLAT>(g < total ? g : total - 1, total, runs, r, c);
+        const int64_t c0 = c * 128 + sub * 8;
         float v[8];
         if (VEC && c0 + 8 <= cols) {
             if (DT == DT_F32) {
@@ -96,16 +113,18 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const void *__restric
 }
 
 // Eight values a thread.
-template <int DT, bool VEC>
+template <int DT, bool VEC, bool FLAT>
 __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t *__restrict__ q,
-                                                             const uint8_t *__restrict__ sc, int64_t rows, int cols,
-                                                             int runs, void *__restrict__ y, int64_t ld) {
-    const int64_t total = rows * runs * 16;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / (runs * 16);
-        const int c0 = (int)(i - r * (runs * 16)) * 8;
-        const uint32_t codes = ((const uint32_t *)q)[i];
-        const uint32_t s = sc[i >> 2];
+                                                             const uint8_t *__restrict__ sc, int64_t rows, int64_t cols,
+                                                             int64_t runs, void *__restrict__ y, int64_t ld) {
+    const int64_t total = rows * runs;
+    const int sub = threadIdx.x & 15;
+    for (int64_t g = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); g < total; g += (int64_t)gridDim.x * 16) {
+        int64_t r, c;
+        mx4_place<FLAT>(g, total, runs, r, c);
+        const int64_t c0 = c * 128 + sub * 8;
+        const uint32_t codes = ((const uint32_t *)q)[g * 16 + sub];
+        const uint32_t s = sc[g * 4 + (sub >> 2)];
         const float unit = s == kNanScale ? __builtin_nanf("") : mx4_unit(s);
         float v[8];
 #pragma unroll
@@ -198,8 +217,8 @@ struct TileList {
     }
     __device__ int start(int e) const { return e ? ends[e - 1] : 0; }
     __device__ int blocks(int e) const { return (ends[e] - start(e) + bm - 1) / bm; }
-    // Tile t < total (the same in all lanes): expert, feature tile, first row and number of rows.  An
-    // expert's rows are split evenly over its blocks.
+    // Tile t < total (the same in all lanes): expert, feature tile, first row and number of rows.  An expert's
+    // token blocks of `unit` rows are split evenly over its row blocks, so that at most one is part empty.
     __device__ void find(int t, int lane, int &e, int &ft, int &row0, int &valid) const {
         const uint64_t started = __ballot(count > 0 && base <= t);
         const int owner = 63 - __builtin_clzll(started);
@@ -218,9 +237,11 @@ struct TileList {
         const int mt = (m + bm - 1) / bm;
         // quotients are vector instructions: back to scalars, which the descriptors have to be
         ft = __builtin_amdgcn_readfirstlane(rest / mt);
-        const int block = rest - ft * mt, mq = __builtin_amdgcn_readfirstlane(m / mt), mr = m - mq * mt;
-        row0 = first + block * mq + min(block, mr);
-        valid = mq + (block < mr ? 1 : 0);
+        const int unit = min(bm, 32), units = (m + unit - 1) / unit;
+        const int block = rest - ft * mt, uq = __builtin_amdgcn_readfirstlane(units / mt), ur = units - uq * mt;
+        const int r = (block * uq + min(block, ur)) * unit;
+        row0 = first + r;
+        valid = min((uq + (block < ur ? 1 : 0)) * unit, m - r);
     }
 };
 
@@ -401,12 +422,13 @@ constexpr int kMx4EndBytes = kMaxExperts * 4;
 // tokens by itself; weights and tokens pass through a ring of segments in LDS that is the wave's own,
 // filled by direct loads and emptied without a barrier, across the ends of tiles.  SPLIT: too few tiles
 // to occupy the GPU; the four waves of a workgroup then share a tile, each a quarter of the segments,
-// and add up in LDS, which leaves room for two segments a wave instead of three.
-constexpr int kMx4SlotBytes = kMx4WeightBytes + 32 * 128;
+// and add up in LDS, which leaves room for 16 tokens.
+constexpr int mx4_stream_tokens(bool split) { return split ? 16 : 32; }
+constexpr int mx4_slot_bytes(bool split) { return kMx4WeightBytes + mx4_stream_tokens(split) * 128; }
 constexpr int kMx4ScaleSlot = (64 + 32) * 16;            // of two segments (WIDE); three of 8 bytes a row fit as well
 constexpr int kMx4PartBytes = (kMx4Waves - 1) * 8 * 64 * 16;
-constexpr int mx4_slots(bool split) { return split ? 2 : 3; }
-constexpr int mx4_wave_lds(bool split) { return mx4_slots(split) * kMx4SlotBytes + 2 * kMx4ScaleSlot; }
+constexpr int kMx4Slots = 3;
+constexpr int mx4_wave_lds(bool split) { return kMx4Slots * mx4_slot_bytes(split) + 2 * kMx4ScaleSlot; }
 constexpr int mx4_stream_lds(bool split) {
     return kMx4EndBytes + kMx4Waves * mx4_wave_lds(split) + (split ? kMx4PartBytes : 0);
 }
@@ -417,14 +439,15 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
     extern __shared__ __align__(16) char smem[];
     const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, r31 = lane & 31;
-    constexpr int SLOTS = mx4_slots(SPLIT), SB = mx4_scale_bytes(WIDE);
-    char *ring = smem + kMx4EndBytes + wid * mx4_wave_lds(SPLIT), *scales = ring + SLOTS * kMx4SlotBytes;
+    constexpr int SLOTS = kMx4Slots, SLOT = mx4_slot_bytes(SPLIT), SB = mx4_scale_bytes(WIDE);
+    constexpr int TOKENS = mx4_stream_tokens(SPLIT);
+    char *ring = smem + kMx4EndBytes + wid * mx4_wave_lds(SPLIT), *scales = ring + SLOTS * SLOT;
     f32x4 *part = (f32x4 *)(smem + kMx4EndBytes + kMx4Waves * mx4_wave_lds(SPLIT));
     mx4_ends(a, (int32_t *)smem);
     // gate/up tiles also cover the padding up to whole runs, which is written as zeros
     const int ftiles = GATEUP ? a.hruns * 4 : (a.F + 63) / 64;
     TileList list;
-    list.init((const int32_t *)smem, a.n_exp, 32, ftiles, lane);
+    list.init((const int32_t *)smem, a.n_exp, TOKENS, ftiles, lane);
     const int segs = (a.kruns + 1) / 2;   // with an odd number of runs the last one has no second half
     // the wave's share of a tile's segments, in pairs where scales come for two
     constexpr int PAIR = WIDE ? 2 : 1;
@@ -435,7 +458,7 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
 
     // the tile and segment whose loads are issued next
     Mx4Weights<WIDE> W;
-    const uint8_t *xp[4], *xsp;
+    const uint8_t *xp[TOKENS / 8], *xsp;
     int it = first, ik = k0, nx = 0, is = 0;
     auto next_tile = [&]() {
         int e, ft, row0, valid;
@@ -447,7 +470,7 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
             return a.gather ? (int64_t)a.gather[R] : R;
         };
 #pragma unroll
-        for (int j = 0; j < 4; ++j) xp[j] = a.x + token(j * 8 + (lane >> 3)) * ((int64_t)a.kruns * 64);
+        for (int j = 0; j < TOKENS / 8; ++j) xp[j] = a.x + token(j * 8 + (lane >> 3)) * ((int64_t)a.kruns * 64);
         xsp = a.xs + token(WIDE ? lane & 31 : lane >> 1) * ((int64_t)a.kruns * 4) + (WIDE ? 0 : (lane & 1) * 4);
         nx = (valid + 7) >> 3;
     };
@@ -458,7 +481,7 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
     auto issue = [&](int slot) {
         if (it >= list.total || k0 >= k1) return 0;
         if (ik == k0) next_tile();
-        char *dst = ring + slot * kMx4SlotBytes, *xd = dst + kMx4WeightBytes;
+        char *dst = ring + slot * SLOT, *xd = dst + kMx4WeightBytes;
         const bool tail = 2 * ik + 1 == a.kruns;
         int n = 8 + nx;
         if (!WIDE || !(ik & 1)) {
@@ -471,7 +494,7 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
         }
         W.load(a, ik, dst, lane);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < TOKENS / 8; ++j) {
             // the half that an odd number of runs lacks meets weights of zero: it repeats the other
             const int p = (lane & 7) ^ mx4_swz(j * 8 + (lane >> 3));
             if (j < nx) dma16(xp[j] + (int64_t)ik * 128 + (tail ? p & 3 : p) * 16, xd + j * 1024);
@@ -483,10 +506,9 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
         return n;
     };
     // loads of the last segments issued
-    int n1 = 0, n2;
     issue(0);
-    if (SLOTS > 2) n1 = issue(1);
-    n2 = issue(SLOTS - 1);
+    int n1 = issue(1), n2 = issue(2);
+    const int column = r31 & (TOKENS - 1);    // further columns of the products repeat the tokens and are not used
     int slot = 0, ss = 0;
     for (int t = first; t < list.total; t += step) {
         f32x16 acc[2] = {};
@@ -494,7 +516,7 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
             // the segment's own loads are done once only the later segments' are outstanding
             wait_vmcnt_dyn(n1 + n2);
             asm volatile("" ::: "memory");
-            const char *src = ring + slot * kMx4SlotBytes, *xsrc = src + kMx4WeightBytes;
+            const char *src = ring + slot * SLOT, *xsrc = src + kMx4WeightBytes;
             const char *sc = scale_slot(ss) + (WIDE && (k & 1) ? 8 : 0) + half * 4;
             if (!WIDE || (k & 1)) ss = after(ss);
             i32x4 w[2][4], x[4];
@@ -502,14 +524,14 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
             for (int c = 0; c < 4; ++c) {
                 w[0][c] = *(const i32x4 *)(src + mx4_lds(r31, half * 4 + c));
                 w[1][c] = *(const i32x4 *)(src + 4096 + mx4_lds(r31, half * 4 + c));
-                x[c] = *(const i32x4 *)(xsrc + mx4_lds(r31, half * 4 + c));
+                x[c] = *(const i32x4 *)(xsrc + mx4_lds(column, half * 4 + c));
             }
             const uint32_t ws0 = *(const uint32_t *)(sc + r31 * SB), ws1 = *(const uint32_t *)(sc + (32 + r31) * SB);
-            const uint32_t xs = *(const uint32_t *)(sc + (64 + r31) * SB);
+            const uint32_t xs = *(const uint32_t *)(sc + (64 + column) * SB);
             wait_lgkm0();                  // the slot has been read: it can be filled again
             asm volatile("" ::: "memory");
             const int n = issue(slot);
-            if (SLOTS > 2) n1 = n2;
+            n1 = n2;
             n2 = n;
             acc[0] = mx4_mfma<0>(w[0][0], x[0], acc[0], ws0, xs);
             acc[1] = mx4_mfma<0>(w[1][0], x[0], acc[1], ws1, xs);
@@ -796,38 +818,44 @@ hipError_t mx4_launch(unsigned grid, int threads, int lds, const Mx4Pass &p, hip
 
 }  // namespace
 
+// f(data type, whether rows take 16-byte accesses, whether the matrix is one row) and the shape for it.
+template <class F>
+static hipError_t mx4_rows_of(int dt, const void *x, int64_t ld, int64_t rows, int64_t cols, F f) {
+    using std::integral_constant;
+    const bool vec = (uintptr_t)x % 16 == 0 && ld % (dt == DT_F32 ? 4 : 8) == 0;
+    const bool flat = vec && ld == cols && cols % 128 == 0;
+    if (flat) {
+        cols *= rows;
+        rows = 1;
+    }
+    const int64_t runs = mx4_runs(cols), wgs = (rows * runs + 15) / 16;
+    const unsigned grid = (unsigned)(wgs < 16384 ? wgs : 16384);
+    auto with = [&](auto dtc) {
+        if (flat) return f(dtc, std::true_type{}, std::true_type{}, grid, rows, cols, runs);
+        if (vec) return f(dtc, std::true_type{}, std::false_type{}, grid, rows, cols, runs);
+        return f(dtc, std::false_type{}, std::false_type{}, grid, rows, cols, runs);
+    };
+    return dt == DT_F32 ? with(integral_constant<int, DT_F32>{}) : with(integral_constant<int, DT_BF16>{});
+}
+
 hipError_t launch_mx4_quantize(int dt, const void *x, int64_t ld, int64_t rows, int cols, uint8_t *q, uint8_t *sc,
                                hipStream_t s) {
     if (rows <= 0) return hipSuccess;
-    const int runs = (int)mx4_runs(cols);
-    const int64_t wgs = (rows * runs + 15) / 16;
-    const unsigned grid = (unsigned)(wgs < 16384 ? wgs : 16384);
-    const bool vec = (uintptr_t)x % 16 == 0 && ld % (dt == DT_F32 ? 4 : 8) == 0;
-    if (dt == DT_F32) {
-        if (vec) mx4_quantize_kernel<DT_F32, true><<<grid, 256, 0, s>>>(x, ld, rows, cols, runs, q, sc);
-        else mx4_quantize_kernel<DT_F32, false><<<grid, 256, 0, s>>>(x, ld, rows, cols, runs, q, sc);
-    } else {
-        if (vec) mx4_quantize_kernel<DT_BF16, true><<<grid, 256, 0, s>>>(x, ld, rows, cols, runs, q, sc);
-        else mx4_quantize_kernel<DT_BF16, false><<<grid, 256, 0, s>>>(x, ld, rows, cols, runs, q, sc);
-    }
-    return hipGetLastError();
+    return mx4_rows_of(dt, x, ld, rows, cols, [&](auto d, auto v, auto f, unsigned grid, int64_t rows, int64_t cols, int64_t runs) {
+        mx4_quantize_kernel<decltype(d)::value, decltype(v)::value, decltype(f)::value>
+            <<<grid, 256, 0, s>>>(x, ld, rows, cols, runs, q, sc);
+        return hipGetLastError();
+    });
 }
 
 hipError_t launch_mx4_dequantize(int dt, const uint8_t *q, const uint8_t *sc, int64_t rows, int cols, void *y,
                                  int64_t ld, hipStream_t s) {
     if (rows <= 0) return hipSuccess;
-    const int runs = (int)mx4_runs(cols);
-    const int64_t wgs = (rows * runs * 16 + 255) / 256;
-    const unsigned grid = (unsigned)(wgs < 16384 ? wgs : 16384);
-    const bool vec = (uintptr_t)y % 16 == 0 && ld % (dt == DT_F32 ? 4 : 8) == 0;
-    if (dt == DT_F32) {
-        if (vec) mx4_dequantize_kernel<DT_F32, true><<<grid, 256, 0, s>>>(q, sc, rows, cols, runs, y, ld);
-        else mx4_dequantize_kernel<DT_F32, false><<<grid, 256, 0, s>>>(q, sc, rows, cols, runs, y, ld);
-    } else {
-        if (vec) mx4_dequantize_kernel<DT_BF16, true><<<grid, 256, 0, s>>>(q, sc, rows, cols, runs, y, ld);
-        else mx4_dequantize_kernel<DT_BF16, false><<<grid, 256, 0, s>>>(q, sc, rows, cols, runs, y, ld);
-    }
-    return hipGetLastError();
+    return mx4_rows_of(dt, y, ld, rows, cols, [&](auto d, auto v, auto f, unsigned grid, int64_t rows, int64_t cols, int64_t runs) {
+        mx4_dequantize_kernel<decltype(d)::value, decltype(v)::value, decltype(f)::value>
+            <<<grid, 256, 0, s>>>(q, sc, rows, cols, runs, y, ld);
+        return hipGetLastError();
+    });
 }
 
 hipError_t launch_mx4_ffn(const Mx4Ffn &a, hipStream_t s) {
