@@ -11,9 +11,10 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (MOE_BF16, MOE_E4M3, MOE_F32, MOE_WS_FORWARD, MoeShape, moe_backward,
-               moe_backward_workspace_bytes, moe_forward, moe_quantize_weights_128x128,
-               moe_transpose_expert_weights, moe_workspace_bytes)
+from . import (MOE_BF16, MOE_E4M3, MOE_F32, MOE_WS_FORWARD, MOE_WS_PERMUTE, MoeShape, make_gate_rule, make_shape,
+               moe_backward, moe_backward_workspace_bytes, moe_combine, moe_dequantize_mx4, moe_ffn_mx4_workspace_bytes,
+               moe_forward, moe_gate, moe_gate_backward, moe_grouped_ffn_mx4, moe_permute, moe_quantize_mx4,
+               moe_quantize_weights_128x128, moe_transpose_expert_weights, moe_workspace_bytes)
 
 
 def to_device(a: np.ndarray, device="cuda") -> torch.Tensor:
@@ -41,6 +42,41 @@ def quantize_weights_128x128(w: torch.Tensor, stream=None):
     dt = MOE_BF16 if w.dtype == torch.bfloat16 else MOE_F32
     moe_quantize_weights_128x128(n, rows, cols, dt, w, q, s, stream)
     return q, s
+
+
+def _float_type(t: torch.Tensor) -> int:
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("bf16 or fp32 expected, not %s" % t.dtype)
+    return MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements from row to row of a matrix whose rows are contiguous (the entry points refuse rows that overlap)."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("a matrix of contiguous rows expected")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def quantize_mx4(x: torch.Tensor, stream=None):
+    """bf16/fp32 device tensor [..., cols] whose rows are contiguous and evenly spaced -> MX4
+    (codes [..., 64 R], scales [..., 4 R]), uint8, R = ceil(cols / 128)."""
+    cols = x.shape[-1]
+    rows = x.view(-1, cols) if x.numel() else x.reshape(0, cols)
+    runs = -(-cols // 128)
+    q = torch.empty(x.shape[:-1] + (64 * runs,), dtype=torch.uint8, device=x.device)
+    s = torch.empty(x.shape[:-1] + (4 * runs,), dtype=torch.uint8, device=x.device)
+    moe_quantize_mx4(rows.shape[0], cols, _float_type(x), rows, _row_stride(rows), q, s, stream)
+    return q, s
+
+
+def dequantize_mx4(q: torch.Tensor, s: torch.Tensor, cols: int, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values [..., cols] that MX4 codes and scales stand for (exact in bf16 and fp32)."""
+    runs = -(-cols // 128)
+    if q.shape[-1] != 64 * runs or s.shape != q.shape[:-1] + (4 * runs,) or not (q.is_contiguous() and s.is_contiguous()):
+        raise ValueError("codes [..., %d] and scales [..., %d], contiguous, expected" % (64 * runs, 4 * runs))
+    y = torch.empty(q.shape[:-1] + (cols,), dtype=dtype, device=q.device)
+    moe_dequantize_mx4(y.numel() // cols, cols, q, s, _float_type(y), y, cols, stream)
+    return y
 
 
 class MoeLayer:
@@ -154,3 +190,82 @@ class MoeLayer:
         moe_backward(self.shape, u, self.gate_w, self.routed_w, self.routed_s, rt, rts, self.shared_w, self.shared_s,
                      st, sts, self._ws, dout, du, dgate_w, d_routed_w, d_shared_w, dtopk_w, self._bws, stream)
         return du
+
+
+class Mx4Experts:
+    """The routed and shared experts of a layer in MX4, behind a gate whose logits the caller computes:
+    choice and weights (moe_gate), dispatch (moe_permute), rounding of the tokens (moe_quantize_mx4), the
+    experts (moe_grouped_ffn_mx4, the shared ones as further experts over all tokens) and moe_combine.
+
+    w_gate, w_up [n][inter][d], w_down [n][d][inter] are bf16 or fp32 device tensors of the n_routed experts
+    and then the n_shared ones; they are rounded once and not kept.  rule: make_gate_rule's keywords beside T,
+    n_experts and topk.  d has to be a multiple of 128, inter may be any size."""
+
+    def __init__(self, w_gate, w_up, w_down, topk, n_shared=0, stream=None, **rule):
+        n, self.inter, self.d = w_gate.shape
+        if w_up.shape != w_gate.shape or w_down.shape != (n, self.d, self.inter) or not 0 <= n_shared < n:
+            raise ValueError("w_gate and w_up [n][inter][d], w_down [n][d][inter] expected, and fewer shared experts than n")
+        self.n_routed, self.n_shared, self.topk, self.rule = n - n_shared, n_shared, topk, rule
+        w = [quantize_mx4(x, stream) for x in (w_gate, w_up, w_down)]
+        self.codes, self.scales = [q for q, _ in w], [s for _, s in w]
+        self._T = -1
+
+    def _gate_rule(self, logits):
+        if logits.shape != (self._T, self.n_routed):
+            raise ValueError("logits [%d][%d] expected" % (self._T, self.n_routed))
+        return make_gate_rule(self._T, self.n_routed, self.topk,
+                              logits="bf16" if _float_type(logits) == MOE_BF16 else "fp32", **self.rule)
+
+    def _buffers(self, T):
+        if T == self._T:
+            return
+        K, Nr, Ns, runs = self.topk, self.n_routed, self.n_shared, -(-self.d // 128)
+        rows, device = T * (K + Ns), self.codes[0].device
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=device)  # noqa: E731
+        # dispatch reads the choice's sizes of it, the combine d as well, neither the experts' inner size
+        self._shape = make_shape(T, self.d, Nr, Ns, 1, 1, K, 128)
+        self.topk_idx, self.topk_w = new((T, K), torch.int32), new((T, K), torch.float32)
+        self.counts = new((Nr,), torch.int32)
+        # the shared experts' rows follow the routed ones': their bounds and tokens never change.  The copies from
+        # the host have ended when these lines return, so that any stream may use them
+        bounds = [0] * Nr + [T * (K + j) for j in range(Ns + 1)]
+        self._offsets = torch.tensor(bounds, dtype=torch.int32).to(device)
+        self._tokens = torch.cat([torch.zeros(T * K, dtype=torch.int32),
+                                  torch.arange(T, dtype=torch.int32).repeat(Ns)]).to(device)
+        self._inv = new((T * K,), torch.int32)
+        self._xq, self._xs = new((T, 64 * runs), torch.uint8), new((T, 4 * runs), torch.uint8)
+        self._y = new((rows, self.d), torch.bfloat16)
+        self._ws = new((moe_ffn_mx4_workspace_bytes(rows, self.inter),), torch.uint8)
+        self._pws = new((max(256, moe_workspace_bytes(self._shape, MOE_WS_PERMUTE)),), torch.uint8)
+        self._T = T
+
+    def forward(self, u: torch.Tensor, logits: torch.Tensor, bias: torch.Tensor = None, out: torch.Tensor = None,
+                scores: torch.Tensor = None, stream=None) -> torch.Tensor:
+        """u [T][d] bf16, logits [T][n_routed] fp32 or bf16 (rows of either may be padded); the choice stays in
+        topk_idx, topk_w and counts.  bias [n_routed] fp32; out [T][d] bf16 and scores [T][n_routed] fp32 contiguous."""
+        T = u.shape[0]
+        if u.dtype != torch.bfloat16 or u.shape[1:] != (self.d,):
+            raise ValueError("u [T][%d] bf16 expected" % self.d)
+        if out is None:
+            out = torch.empty((T, self.d), dtype=u.dtype, device=u.device)
+        if T == 0:
+            return out
+        self._buffers(T)
+        moe_gate(self._gate_rule(logits), logits, _row_stride(logits), bias, scores, self.topk_idx, self.topk_w, stream)
+        moe_permute(self._shape, self.topk_idx, None, self.counts, self._offsets, self._tokens, self._inv, None, None,
+                    self._pws, stream)
+        moe_quantize_mx4(T, self.d, MOE_BF16, u, _row_stride(u), self._xq, self._xs, stream)
+        moe_grouped_ffn_mx4(self.n_routed + self.n_shared, self._offsets, T * (self.topk + self.n_shared), self._tokens,
+                            self.d, self.inter, self._xq, self._xs, self.codes, self.scales, self._y, self._ws, stream)
+        shared = self._y[T * self.topk:] if self.n_shared else None
+        moe_combine(self._shape, self._y, self._inv, self.topk_w, shared, None, out, stream)
+        return out
+
+    def gate_gradient(self, logits: torch.Tensor, dtopk_w: torch.Tensor, dscores: torch.Tensor = None,
+                      stream=None) -> torch.Tensor:
+        """dL/dlogits of the most recent forward's choice, from dL/dtopk_w and (optional) dL/dscores."""
+        rule = self._gate_rule(logits)
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        moe_gate_backward(rule, logits, _row_stride(logits), self.topk_idx, self.topk_w, dtopk_w, dscores, dlogits,
+                          self.n_routed, stream)
+        return dlogits

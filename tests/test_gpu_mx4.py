@@ -165,6 +165,16 @@ SHAPES = [
     ([5] * 40 + [0] * 30, 96, 31),
     ([4, 3], 31, 1),
     ([4, 40], 1, 5),
+    # scales in pieces of two segments: waves sharing a tile, waves by themselves, tiles of up to 128 and 160 tokens
+    ([1, 0, 16, 2], 1024, 512),
+    ([2] * 40, 512, 512),
+    ([17, 1, 0, 40, 33], 1024, 512),
+    ([3, 500, 129, 2], 512, 512),
+    ([120, 140, 160, 129, 161, 31], 512, 512),
+    # the same kernels with scales by words
+    ([1] * 60, 384, 640),
+    ([150, 97], 130, 97),
+    ([150, 128, 159, 1, 260], 384, 640),
 ]
 
 
