@@ -304,7 +304,7 @@ struct Mx4Weights {
         }
     }
     // Codes of segment k.  Rows that this tile alone reads (an expert of one row block) are loaded with the
-    // nontemporal policy, so that L2 keeps the tokens: decode batch 999 -> 928 us.
+    // nontemporal policy, so that L2 keeps the tokens: 256 experts of 7168 x 2048, 4 rows each, 928 us against 999.
     __device__ __forceinline__ void load(const Mx4Pass &a, int k, char *dst, int lane) const {
         const bool tail = 2 * k + 1 == a.kruns;
         auto each = [&](auto once) {
@@ -418,11 +418,12 @@ __device__ __forceinline__ void mx4_ends(const Mx4Pass &a, int32_t *o) {
 }
 constexpr int kMx4EndBytes = kMaxExperts * 4;
 
-// Few rows an expert: bound by the stream of weights.  A wave takes tiles of 64 weight rows and up to 32
-// tokens by itself; weights and tokens pass through a ring of segments in LDS that is the wave's own,
-// filled by direct loads and emptied without a barrier, across the ends of tiles.  SPLIT: too few tiles
-// to occupy the GPU; the four waves of a workgroup then share a tile, each a quarter of the segments,
-// and add up in LDS, which leaves room for 16 tokens.
+// Few tiles: bound by the time from one load to the next in each wave, so the work is cut finely.  A wave takes tiles
+// of 64 weight rows and up to 32 tokens by itself; weights and tokens pass through a ring of segments in LDS that is
+// the wave's own, filled by direct loads and emptied without a barrier, across the ends of tiles.  SPLIT: the four
+// waves of a workgroup share a tile, each a quarter of the segments, and add up in LDS, in the order of the waves,
+// which leaves room for 16 tokens.  One token, 8 experts of 7168 x 2048: gate/up 25 us, down 14 us (187 MB of
+// weights at 4.8 TB/s).
 constexpr int mx4_stream_tokens(bool split) { return split ? 16 : 32; }
 constexpr int mx4_slot_bytes(bool split) { return kMx4WeightBytes + mx4_stream_tokens(split) * 128; }
 constexpr int kMx4ScaleSlot = (64 + 32) * 16;            // of two segments (WIDE); three of 8 bytes a row fit as well
@@ -573,13 +574,18 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
     }
 }
 
-// Many rows an expert.  A workgroup's tile is 256 weight rows against up to CAP blocks of 32 tokens.  Four waves, one a
+// Many tiles.  A workgroup's tile is 256 weight rows against up to CAP blocks of 32 tokens.  Four waves, one a
 // SIMD, multiply (64 weight rows each, all tokens); four others, one a SIMD too, only bring segments into rings in
 // LDS, across the ends of tiles, so that no product waits behind a load that finds the memory pipeline full.  One
 // barrier a segment: passing it, a segment's loads are done and the places of the segment before have been read.
 // CAP 4 leaves room for three segments of weights and of tokens.  CAP 5 leaves room for two of tokens, which come from L2
 // and arrive in time beside weights from memory; it is for experts of about 128 rows, most of which then need
 // one tile and read their weights once.
+//
+// 256 experts of 7168 x 2048: at 4 rows each bound by the stream of weights (5.98 GB in 890 us, 6.7 TB/s), at 128 rows by
+// the stream and the products together (gate/up 910 us, down 500), neither of which the other's waits fill whole.
+// 32 experts, 512 rows: products (gate/up 350 us, 2.7 of 6.7 PFLOP/s), the loads from L2 into LDS that feed them (8 of
+// 16 TB/s) and the epilogue, which the multiplying waves do not overlap.
 constexpr int kMx4TileThreads = 512;
 constexpr int kMx4WeightStages = 3;
 constexpr int mx4_token_stages(int cap) { return cap <= 4 ? 3 : 2; }
@@ -885,23 +891,33 @@ hipError_t launch_mx4_ffn(const Mx4Ffn &a, hipStream_t s) {
     down.yvec = (uintptr_t)a.y % 16 == 0 && a.d % 8 == 0;
     const int64_t cus = device_cus();
     const unsigned grid = (unsigned)((cus + 7) / 8 * 8);
-    // Up to 16 rows an expert on average a tile is bound by its weights, whose stream the per-wave rings keep
-    // up best (256 experts of 7168 x 2048: 917 us at 4 rows, where the tile kernel has half its places empty;
-    // at 20 rows 1118 us against the tile kernel's 1030, at 60 rows 1850 against 1210).
-    const bool few = a.max_rows <= 16 * (int64_t)a.n_exp;
-    // Four waves share a tile where the experts' tiles would not give half the waves one: one token, 8 of
-    // those experts: gate/up (512 tiles) 24 us against 30, down (896 tiles) 20 against 13 without sharing.
     const int64_t experts = a.max_rows < a.n_exp ? a.max_rows : a.n_exp;
-    // One tile instead of two for most experts of 112 to 160 rows: 128 rows on average 1430 us against 1560;
-    // outside, three stages of tokens do better (97 rows of a small, skewed case 22 us against 24).
-    const bool tall = a.max_rows > 112 * (int64_t)a.n_exp && a.max_rows <= 160 * (int64_t)a.n_exp;
-    auto pass = [&](auto gateup, auto wide, const Mx4Pass &p, int64_t tiles) {
+    // row blocks of bm rows, at most
+    auto blocks = [&](int64_t bm) { return experts + (a.max_rows - experts) / bm; };
+    auto pass = [&](auto gateup, auto wide, const Mx4Pass &p, int64_t ftiles) {
         constexpr bool GU = decltype(gateup)::value, W = decltype(wide)::value;
-        if (!few && tall) return mx4_launch<mx4_tile_kernel<GU, W, 5>>(grid, kMx4TileThreads, mx4_tile_lds(5), p, s);
-        if (!few) return mx4_launch<mx4_tile_kernel<GU, W, 4>>(grid, kMx4TileThreads, mx4_tile_lds(4), p, s);
-        if (experts * tiles <= 2 * cus)
+        // Four waves share a tile where that ends sooner: `rounds` tiles a workgroup, one after the other, each a
+        // quarter of the segments and, for adding up, as long as 2.5 more, against all segments by one wave.  With
+        // rows of 7168 (28 segments) and 2048 (8), experts of 7168 x 2048: 1 token to 8 experts, gate/up in 2 rounds
+        // shared 42 us (the whole call), not shared 50; 32 tokens of one expert, down in 1 round 23 against 26,
+        // 48 tokens in 2 rounds 28 against 26.
+        const int64_t segs = (p.kruns + 1) / 2, rounds = (blocks(mx4_stream_tokens(true)) * ftiles + cus - 1) / cus;
+        if (rounds * (segs + 10) < 4 * segs)
             return mx4_launch<mx4_stream_kernel<GU, true, W>>(grid, kMx4Threads, mx4_stream_lds(true), p, s);
-        return mx4_launch<mx4_stream_kernel<GU, false, W>>(grid, kMx4Threads, mx4_stream_lds(false), p, s);
+        // Tiles for a wave by itself as long as there is no more than one for each wave: one expert of 7168 x 2048,
+        // 384 tokens, gate/up of 768 tiles 42 us (the whole call) against 52 in the tile kernel, 640 tokens, 1280 tiles
+        // 65 against 53; 8 x 512 tokens of 512 x 256, 1024 tiles in either pass 16 against 22.
+        if (blocks(mx4_stream_tokens(false)) * ftiles <= cus * kMx4Waves)
+            return mx4_launch<mx4_stream_kernel<GU, false, W>>(grid, kMx4Threads, mx4_stream_lds(false), p, s);
+        // Tiles of up to 160 tokens where experts of the average size need fewer of them than of 128 (an eighth is
+        // left for experts above the average) and there is one for each workgroup.  256 experts of 7168 x 2048:
+        // 90 rows 1290 us either way, 128 rows 1410 us against 1540 with 128 tokens, 219 rows 2430 against 2100,
+        // 256 rows 2330 against 2430; 8 experts of 2048 x 1024, 128 rows, 64 tiles: 33 against 30.
+        const int64_t n = a.n_exp;
+        const bool fewer = (a.max_rows + 140 * n - 1) / (140 * n) < (a.max_rows + 112 * n - 1) / (112 * n);
+        if (fewer && blocks(160) * ((ftiles + 3) / 4) >= cus)
+            return mx4_launch<mx4_tile_kernel<GU, W, 5>>(grid, kMx4TileThreads, mx4_tile_lds(5), p, s);
+        return mx4_launch<mx4_tile_kernel<GU, W, 4>>(grid, kMx4TileThreads, mx4_tile_lds(4), p, s);
     };
     auto either = [&](auto gateup, const Mx4Pass &p, int64_t tiles) {
         const uintptr_t all = (uintptr_t)p.xs | (uintptr_t)p.s0 | (uintptr_t)p.s1;
