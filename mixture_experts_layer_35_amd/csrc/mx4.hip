@@ -39,7 +39,7 @@ __device__ __forceinline__ uint32_t mx4_codes(const float (&v)[8], uint32_t s) {
 }
 
 // Row and run of run g of a matrix of rows of `runs` runs.  FLAT: the rows are whole runs without gaps, so the
-// matrix is one row (the division of 64-bit indices took longer than the memory).
+// matrix is one row (16384 x 7168 there and back 2 % less time than with a division for each run).
 template <bool FLAT>
 __device__ __forceinline__ void mx4_place(int64_t g, int64_t total, int64_t runs, int64_t &r, int64_t &c) {
     if (FLAT) {
@@ -55,7 +55,10 @@ __device__ __forceinline__ void mx4_place(int64_t g, int64_t total, int64_t runs
     }
 }
 
-// 16 lanes per run of 128 values, eight values a lane, four lanes a block.
+// 16 lanes per run of 128 values, eight values a lane (one 16-byte load of bf16), four lanes a block, whose largest
+// magnitude takes two lane exchanges; a run's codes are one whole line of 64 bytes.  Bound by memory: 16384 x 7168 bf16
+// to codes 49 us, 297 MB, 6.1 TB/s.  The values are read once, and nontemporal loads keep them from displacing what the
+// caches hold: 60 us without.
 template <int DT, bool VEC, bool FLAT>
 __global__ __launch_bounds__(256) void mx4_quantize_kernel(const void *__restrict__ x, int64_t ld, int64_t rows,
                                                            int64_t cols, int64_t runs, uint8_t *__restrict__ q,
@@ -72,14 +75,14 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const void *__restric
         if (VEC && c0 + 8 <= cols) {
             if (DT == DT_F32) {
                 const f32x4 *p = (const f32x4 *)((const float *)x + r * ld + c0);
-                const f32x4 a = p[0], b = p[1];
+                const f32x4 a = __builtin_nontemporal_load(p), b = __builtin_nontemporal_load(p + 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     v[i] = a[i];
                     v[4 + i] = b[i];
                 }
             } else {
-                const u32x4 a = *(const u32x4 *)((const uint16_t *)x + r * ld + c0);
+                const u32x4 a = __builtin_nontemporal_load((const u32x4 *)((const uint16_t *)x + r * ld + c0));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     v[2 * i] = __uint_as_float(a[i] << 16);
@@ -112,7 +115,8 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const void *__restric
     }
 }
 
-// Eight values a thread.
+// Eight values a thread.  Bound by memory: 16384 x 7168 codes to bf16 49 us, 297 MB, 6.0 TB/s, four fifths of it
+// writing, by nontemporal stores: 73 us without.
 template <int DT, bool VEC, bool FLAT>
 __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t *__restrict__ q,
                                                              const uint8_t *__restrict__ sc, int64_t rows, int64_t cols,
@@ -137,11 +141,13 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t *__re
         if (VEC && c0 + 8 <= cols) {
             if (DT == DT_F32) {
                 f32x4 *p = (f32x4 *)((float *)y + r * ld + c0);
-                p[0] = f32x4{v[0], v[1], v[2], v[3]};
-                p[1] = f32x4{v[4], v[5], v[6], v[7]};
+                const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+                __builtin_nontemporal_store(lo, p);
+                __builtin_nontemporal_store(hi, p + 1);
             } else {
-                *(u32x4 *)((uint16_t *)y + r * ld + c0) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+                const u32x4 o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                 pack_bf16x2(v[6], v[7])};
+                __builtin_nontemporal_store(o, (u32x4 *)((uint16_t *)y + r * ld + c0));
             }
         } else {
 #pragma unroll
