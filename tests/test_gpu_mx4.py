@@ -175,6 +175,11 @@ SHAPES = [
     ([1] * 60, 384, 640),
     ([150, 97], 130, 97),
     ([150, 128, 159, 1, 260], 384, 640),
+    # enough tiles for the kernel of whole workgroups: of up to 128 tokens, and (averages of 130) of up to 160
+    ([40] * 40, 1024, 1024),
+    ([33, 1, 0, 64, 500, 129] * 4, 700, 700),
+    ([97, 161, 130, 132, 159, 160, 1, 200] * 2, 2304, 2048),
+    ([128, 130, 129, 131, 150, 96, 192, 84] * 2, 2300, 2100),
 ]
 
 
