@@ -457,6 +457,9 @@ int moe_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t *q, const uint8
  * for the rows r in [offsets[e], offsets[e+1]) of expert e, x_r = x[gather[r]]
  * (gather NULL: x[r]); Q is moe_quantize_mx4's rounding of the fp32 values;
  * products of codes and scales are summed in fp32; y [max_rows][d] is bf16.
+ * Deterministic: no sum's order changes from call to call.  max_rows, n_exp, d and
+ * inter choose it, so a row among more rows can differ in the last bit of a sum
+ * (and, where that meets a rounding boundary, by a code of h).
  * n_exp <= 1024 experts; offsets [n_exp+1] int32 on the device, offsets[0] = 0,
  * non-decreasing, offsets[n_exp] <= max_rows.  d and inter are any positive
  * sizes (rows padded to whole runs as above).

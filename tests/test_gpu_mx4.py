@@ -205,8 +205,7 @@ def test_no_rows(moe):
     assert moe.moe_grouped_ffn_mx4(2, 0, 0, None, 128, 32, 0, 0, None, None, 0, None) == 0
 
 
-def test_same_bits_each_time_and_for_a_row_alone(moe):
-    # a row's result depends on neither its neighbours nor the run
+def test_same_bits_each_time(moe):
     counts, d, inter = [40, 0, 3, 90], 512, 192
     torch.manual_seed(9)
     x = torch.randn(133, d, dtype=torch.float64)
