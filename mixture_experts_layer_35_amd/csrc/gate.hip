@@ -192,7 +192,7 @@ __device__ __forceinline__ void store_row(void *row, int l, int n, bool vec, con
 }
 
 struct GateArgs {
-    int64_t T, ld, dld;
+    int64_t T, ld, dld, t0;   // t0: the launch's first token
     int E, G, M, K;
     bool softmax, renorm, group_max;
     // whether rows of the logits, of scores / ds, of dlogits and the bias take four-value accesses
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs a) {
     uint32_t *ckey = (uint32_t *)(sval + (bias ? E4 : 0));
     uint32_t *gkey = ckey + E + G;
     // the wave's tokens past T work on the last one and store nothing
-    const int64_t t0 = (int64_t)blockIdx.x * TPB + sub;
+    const int64_t t0 = a.t0 + (int64_t)blockIdx.x * TPB + sub;
     const bool live = t0 < a.T;
     const int64_t t = live ? t0 : a.T - 1;
     const char *row = (const char *)a.logits + t * a.ld * (DT == DT_F32 ? 4 : 2);
@@ -505,7 +505,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(const GateA
     const int sub = threadIdx.x / L, l = threadIdx.x % L;
     const int E = a.E, K = a.K;
     float *dsl = (float *)(lds + sub * gate_backward_lds_words(E));   // the slots' part of s ds, or of dz
-    const int64_t t0 = (int64_t)blockIdx.x * TPB + sub;
+    const int64_t t0 = a.t0 + (int64_t)blockIdx.x * TPB + sub;
     const bool live = t0 < a.T;
     const int64_t t = live ? t0 : a.T - 1;
     const char *row = (const char *)a.logits + t * a.ld * (DT == DT_F32 ? 4 : 2);
@@ -630,6 +630,19 @@ hipError_t with_width(int64_t T, int E, F f) {
     return f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
 }
 
+// A launch holds fewer than 2^32 threads: f(first token, grid) for parts of the batch of TPB tokens a workgroup.
+template <class F>
+hipError_t in_launches(int64_t T, int TPB, F f) {
+    const int64_t part = (int64_t)((1ll << 32) / kGateThreads - 1) * TPB;
+    for (int64_t t = 0; t < T; t += part) {
+        const int64_t n = T - t < part ? T - t : part;
+        f(t, (unsigned)((n + TPB - 1) / TPB));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 // Whether every row of a matrix can be read four values at a time.
 bool rows_of_four(const void *p, int64_t ld, int esz) { return (uintptr_t)p % (4 * esz) == 0 && ld % 4 == 0; }
 
@@ -663,11 +676,12 @@ hipError_t launch_gate(const GateProblem &p, const float *bias, float *scores, i
     a.w = w;
     return with_width(p.T, p.E, [&](auto lc, auto vc) {
         constexpr int L = decltype(lc)::value, V = decltype(vc)::value, TPB = kGateThreads / L;
-        const unsigned grid = (unsigned)((p.T + TPB - 1) / TPB);
         const size_t lds = (size_t)TPB * gate_lds_words(p.E, p.G, bias != nullptr) * 4;
-        if (p.dt == DT_F32) gate_kernel<DT_F32, L, V><<<grid, kGateThreads, lds, s>>>(a);
-        else gate_kernel<DT_BF16, L, V><<<grid, kGateThreads, lds, s>>>(a);
-        return hipGetLastError();
+        return in_launches(p.T, TPB, [&](int64_t t, unsigned grid) {
+            a.t0 = t;
+            if (p.dt == DT_F32) gate_kernel<DT_F32, L, V><<<grid, kGateThreads, lds, s>>>(a);
+            else gate_kernel<DT_BF16, L, V><<<grid, kGateThreads, lds, s>>>(a);
+        });
     });
 }
 
@@ -685,17 +699,18 @@ hipError_t launch_gate_backward(const GateProblem &p, const int32_t *idx, const 
     a.dvec = rows_of_four(dlogits, dld, p.dt == DT_F32 ? 4 : 2);
     return with_width(p.T, p.E, [&](auto lc, auto vc) {
         constexpr int L = decltype(lc)::value, V = decltype(vc)::value, TPB = kGateThreads / L;
-        const unsigned grid = (unsigned)((p.T + TPB - 1) / TPB);
         const size_t lds = (size_t)TPB * gate_backward_lds_words(p.E) * 4;
         const bool dense = p.softmax || ds;
-        if (p.dt == DT_F32) {
-            if (dense) gate_backward_kernel<DT_F32, L, V, true><<<grid, kGateThreads, lds, s>>>(a);
-            else gate_backward_kernel<DT_F32, L, V, false><<<grid, kGateThreads, lds, s>>>(a);
-        } else {
-            if (dense) gate_backward_kernel<DT_BF16, L, V, true><<<grid, kGateThreads, lds, s>>>(a);
-            else gate_backward_kernel<DT_BF16, L, V, false><<<grid, kGateThreads, lds, s>>>(a);
-        }
-        return hipGetLastError();
+        return in_launches(p.T, TPB, [&](int64_t t, unsigned grid) {
+            a.t0 = t;
+            if (p.dt == DT_F32) {
+                if (dense) gate_backward_kernel<DT_F32, L, V, true><<<grid, kGateThreads, lds, s>>>(a);
+                else gate_backward_kernel<DT_F32, L, V, false><<<grid, kGateThreads, lds, s>>>(a);
+            } else {
+                if (dense) gate_backward_kernel<DT_BF16, L, V, true><<<grid, kGateThreads, lds, s>>>(a);
+                else gate_backward_kernel<DT_BF16, L, V, false><<<grid, kGateThreads, lds, s>>>(a);
+            }
+        });
     });
 }
 
