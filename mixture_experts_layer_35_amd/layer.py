@@ -8,6 +8,8 @@ the device by ``moe_quantize_weights_128x128`` (128 x 128 blocks, §3.3 of the
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -15,6 +17,7 @@ from . import (MOE_BF16, MOE_E4M3, MOE_F32, MOE_WS_FORWARD, MOE_WS_PERMUTE, MoeS
                moe_backward, moe_backward_workspace_bytes, moe_combine, moe_dequantize_mx4, moe_ffn_mx4_workspace_bytes,
                moe_forward, moe_gate, moe_gate_backward, moe_grouped_ffn_mx4, moe_permute, moe_quantize_mx4,
                moe_quantize_weights_128x128, moe_transpose_expert_weights, moe_workspace_bytes)
+from . import _stream as _raw
 
 
 def to_device(a: np.ndarray, device="cuda") -> torch.Tensor:
@@ -44,6 +47,20 @@ def quantize_weights_128x128(w: torch.Tensor, stream=None):
     return q, s
 
 
+def _torch_stream(stream, device) -> torch.cuda.Stream:
+    """The torch stream of what the entry points take as one (a torch stream, a handle, None)."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, int):
+        return torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    return stream
+
+
+def _on(stream, device):
+    """What is allocated inside belongs to `stream`: once dropped, its memory is reused behind that stream's work alone."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream, device))
+
+
 def _float_type(t: torch.Tensor) -> int:
     if t.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("bf16 or fp32 expected, not %s" % t.dtype)
@@ -63,8 +80,9 @@ def quantize_mx4(x: torch.Tensor, stream=None):
     cols = x.shape[-1]
     rows = x.view(-1, cols) if x.numel() else x.reshape(0, cols)
     runs = -(-cols // 128)
-    q = torch.empty(x.shape[:-1] + (64 * runs,), dtype=torch.uint8, device=x.device)
-    s = torch.empty(x.shape[:-1] + (4 * runs,), dtype=torch.uint8, device=x.device)
+    with _on(stream, x.device):
+        q = torch.empty(x.shape[:-1] + (64 * runs,), dtype=torch.uint8, device=x.device)
+        s = torch.empty(x.shape[:-1] + (4 * runs,), dtype=torch.uint8, device=x.device)
     moe_quantize_mx4(rows.shape[0], cols, _float_type(x), rows, _row_stride(rows), q, s, stream)
     return q, s
 
@@ -74,7 +92,8 @@ def dequantize_mx4(q: torch.Tensor, s: torch.Tensor, cols: int, dtype=torch.bflo
     runs = -(-cols // 128)
     if q.shape[-1] != 64 * runs or s.shape != q.shape[:-1] + (4 * runs,) or not (q.is_contiguous() and s.is_contiguous()):
         raise ValueError("codes [..., %d] and scales [..., %d], contiguous, expected" % (64 * runs, 4 * runs))
-    y = torch.empty(q.shape[:-1] + (cols,), dtype=dtype, device=q.device)
+    with _on(stream, q.device):
+        y = torch.empty(q.shape[:-1] + (cols,), dtype=dtype, device=q.device)
     moe_dequantize_mx4(y.numel() // cols, cols, q, s, _float_type(y), y, cols, stream)
     return y
 
@@ -199,7 +218,12 @@ class Mx4Experts:
 
     w_gate, w_up [n][inter][d], w_down [n][d][inter] are bf16 or fp32 device tensors of the n_routed experts
     and then the n_shared ones; they are rounded once and not kept.  rule: make_gate_rule's keywords beside T,
-    n_experts and topk.  d has to be a multiple of 128, inter may be any size."""
+    n_experts and topk.  d has to be a multiple of 128, inter may be any size.
+
+    Buffers hold the largest batch so far and are shared by all calls: calls on different streams have to be ordered by
+    the caller, as for every workspace, and topk_idx, topk_w and counts hold the last call's choice.  A call's results
+    belong to its stream.  A graph that captures a call keeps the buffers' addresses: run the largest batch before
+    capturing."""
 
     def __init__(self, w_gate, w_up, w_down, topk, n_shared=0, stream=None, **rule):
         n, self.inter, self.d = w_gate.shape
@@ -208,7 +232,8 @@ class Mx4Experts:
         self.n_routed, self.n_shared, self.topk, self.rule = n - n_shared, n_shared, topk, rule
         w = [quantize_mx4(x, stream) for x in (w_gate, w_up, w_down)]
         self.codes, self.scales = [q for q, _ in w], [s for _, s in w]
-        self._T = -1
+        self._T, self._capacity, self._held = -1, 0, None
+        self._streams = {_raw(stream)}     # those that own the weights and buffers or were recorded on them
 
     def _gate_rule(self, logits):
         if logits.shape != (self._T, self.n_routed):
@@ -216,27 +241,50 @@ class Mx4Experts:
         return make_gate_rule(self._T, self.n_routed, self.topk,
                               logits="bf16" if _float_type(logits) == MOE_BF16 else "fp32", **self.rule)
 
-    def _buffers(self, T):
-        if T == self._T:
-            return
+    def _use(self, stream):
+        """Before work on `stream`: weights and buffers that are dropped later are not reused before it has ended."""
+        if _raw(stream) not in self._streams:
+            for t in self.codes + self.scales + list(self._held or ()):
+                t.record_stream(_torch_stream(stream, t.device))
+            self._streams.add(_raw(stream))
+
+    def _buffers(self, T, stream):
+        """Buffers for T tokens on `stream`."""
         K, Nr, Ns, runs = self.topk, self.n_routed, self.n_shared, -(-self.d // 128)
-        rows, device = T * (K + Ns), self.codes[0].device
-        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=device)  # noqa: E731
-        # dispatch reads the choice's sizes of it, the combine d as well, neither the experts' inner size
-        self._shape = make_shape(T, self.d, Nr, Ns, 1, 1, K, 128)
-        self.topk_idx, self.topk_w = new((T, K), torch.int32), new((T, K), torch.float32)
-        self.counts = new((Nr,), torch.int32)
-        # the shared experts' rows follow the routed ones': their bounds and tokens never change.  The copies from
-        # the host have ended when these lines return, so that any stream may use them
-        bounds = [0] * Nr + [T * (K + j) for j in range(Ns + 1)]
-        self._offsets = torch.tensor(bounds, dtype=torch.int32).to(device)
-        self._tokens = torch.cat([torch.zeros(T * K, dtype=torch.int32),
-                                  torch.arange(T, dtype=torch.int32).repeat(Ns)]).to(device)
-        self._inv = new((T * K,), torch.int32)
-        self._xq, self._xs = new((T, 64 * runs), torch.uint8), new((T, 4 * runs), torch.uint8)
-        self._y = new((rows, self.d), torch.bfloat16)
-        self._ws = new((moe_ffn_mx4_workspace_bytes(rows, self.inter),), torch.uint8)
-        self._pws = new((max(256, moe_workspace_bytes(self._shape, MOE_WS_PERMUTE)),), torch.uint8)
+        device = self.codes[0].device
+        self._use(stream)
+        if T > self._capacity:
+            # the old ones are released before the larger ones are taken
+            self._T, self._capacity, self._held = -1, 0, None
+            self.topk_idx = self.topk_w = self.counts = self._offsets = self._tokens = self._inv = None
+            self._xq = self._xs = self._y = self._ws = self._pws = None
+            shape = make_shape(T, self.d, Nr, Ns, 1, 1, K, 128)
+            with _on(stream, device):
+                new = lambda n, dtype: torch.empty(n, dtype=dtype, device=device)  # noqa: E731
+                rows = T * (K + Ns)
+                self._held = (new((T, K), torch.int32), new((T, K), torch.float32), new((Nr,), torch.int32),
+                              new((Nr + Ns + 1,), torch.int32), new((rows,), torch.int32), new((T * K,), torch.int32),
+                              new((T, 64 * runs), torch.uint8), new((T, 4 * runs), torch.uint8),
+                              new((rows, self.d), torch.bfloat16),
+                              new((moe_ffn_mx4_workspace_bytes(rows, self.inter),), torch.uint8),
+                              new((max(256, moe_workspace_bytes(shape, MOE_WS_PERMUTE)),), torch.uint8))
+            self._capacity, self._streams = T, {_raw(stream)}
+        if T != self._T:
+            idx, w, counts, offsets, tokens, inv, xq, xs, y, ws, pws = self._held
+            rows = T * (K + Ns)
+            # dispatch reads the choice's sizes of it, the combine d as well, neither the experts' inner size
+            self._shape = make_shape(T, self.d, Nr, Ns, 1, 1, K, 128)
+            self.topk_idx, self.topk_w, self.counts, self._offsets = idx[:T], w[:T], counts, offsets
+            self._tokens, self._inv, self._xq, self._xs = tokens[:rows], inv[:T * K], xq[:T], xs[:T]
+            self._y, self._ws, self._pws = y[:rows], ws, pws
+        if Ns:
+            # the shared experts' rows follow the routed ones'; a graph writes their bounds and tokens itself, since other
+            # batches may come between its replays
+            with _on(stream, device):
+                if T != self._T or torch.cuda.is_current_stream_capturing():
+                    torch.arange(T * K, T * (K + Ns) + 1, T, out=self._offsets[Nr:])
+                    for j in range(Ns):
+                        torch.arange(T, out=self._tokens[T * (K + j):T * (K + j + 1)])
         self._T = T
 
     def forward(self, u: torch.Tensor, logits: torch.Tensor, bias: torch.Tensor = None, out: torch.Tensor = None,
@@ -247,10 +295,11 @@ class Mx4Experts:
         if u.dtype != torch.bfloat16 or u.shape[1:] != (self.d,):
             raise ValueError("u [T][%d] bf16 expected" % self.d)
         if out is None:
-            out = torch.empty((T, self.d), dtype=u.dtype, device=u.device)
+            with _on(stream, u.device):
+                out = torch.empty((T, self.d), dtype=u.dtype, device=u.device)
         if T == 0:
             return out
-        self._buffers(T)
+        self._buffers(T, stream)
         moe_gate(self._gate_rule(logits), logits, _row_stride(logits), bias, scores, self.topk_idx, self.topk_w, stream)
         moe_permute(self._shape, self.topk_idx, None, self.counts, self._offsets, self._tokens, self._inv, None, None,
                     self._pws, stream)
@@ -265,7 +314,9 @@ class Mx4Experts:
                       stream=None) -> torch.Tensor:
         """dL/dlogits of the most recent forward's choice, from dL/dtopk_w and (optional) dL/dscores."""
         rule = self._gate_rule(logits)
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        self._use(stream)
+        with _on(stream, logits.device):
+            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
         moe_gate_backward(rule, logits, _row_stride(logits), self.topk_idx, self.topk_w, dtopk_w, dscores, dlogits,
                           self.n_routed, stream)
         return dlogits

@@ -1,0 +1,117 @@
+"""Mx4Experts and the MX4 helpers on streams of their own: batches of changing sizes queued without waiting give the
+bits of calls that are waited for, whatever the current stream allocates and writes meanwhile."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+SIZES = (1, 16, 1500, 1, 1501, 16, 4096, 4096, 1, 16)
+D, INTER, NR, NS, K = 256, 96, 16, 2, 3
+
+
+def build(stream=None):
+    from mixture_experts_layer_35_amd.layer import Mx4Experts
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = [torch.randn(s, device="cuda", generator=g) * 0.1 for s in ((NR + NS, INTER, D), (NR + NS, INTER, D), (NR + NS, D, INTER))]
+    torch.cuda.synchronize()
+    layer = Mx4Experts(*w, K, NS, stream=stream, score="softmax", n_groups=4, topk_groups=2)
+    torch.cuda.synchronize()
+    return layer
+
+
+def inputs(seed, T):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *s: torch.randn(s, device="cuda", generator=g)  # noqa: E731
+    return rand(T, D).to(torch.bfloat16), rand(T, NR), rand(T, K), rand(T, NR)
+
+
+def results(layer, x, stream, out=None):
+    u, z, dw, ds = x
+    y = layer.forward(u, z, out=out, stream=stream)
+    return y, layer.gate_gradient(z, dw, ds, stream=stream)
+
+
+@pytest.fixture(scope="module")
+def expected():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    layer, want = build(), []
+    for i, T in enumerate(SIZES):
+        got = results(layer, inputs(i, T), None)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in got + (layer.topk_idx, layer.topk_w, layer.counts)])
+        assert int(layer.counts.sum()) == T * K
+    return want
+
+
+def trample(sizes):
+    """What the current stream's allocator hands out, overwritten at once."""
+    for n in sizes:
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xFF)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_batches_of_changing_sizes_without_waiting(expected, handle):
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    xs = [inputs(i, T) for i, T in enumerate(SIZES)]
+    torch.cuda.synchronize()
+    for rep in range(3):
+        layer = build(stream)
+        got = []
+        for x, T in zip(xs, SIZES):
+            got.append(results(layer, x, stream))
+            trample([4 * T * K, 4 * NR, T * D, 2 * T * (K + NS) * D, T * 64 * 2, 4 * T * (K + NS)])
+        del layer                                              # the weights too are dropped while work is queued
+        trample([(NR + NS) * INTER * D // 2, (NR + NS) * D * 64])
+        torch.cuda.synchronize()
+        for a, b in zip(got, expected):
+            assert (a[0] == b[0]).all() and (a[1] == b[1]).all()
+
+
+def test_streams_in_turn(expected):
+    streams = [None, torch.cuda.Stream(), torch.cuda.Stream()]
+    layer = build()
+    for i, T in enumerate(SIZES):
+        s = streams[i % 3]
+        x = inputs(i, T)
+        torch.cuda.synchronize()
+        y, dz = results(layer, x, s)
+        trample([4 * T * K, 4 * NR, 2 * T * (K + NS) * D])
+        torch.cuda.synchronize()
+        assert all((a == b).all() for a, b in zip((y, dz, layer.topk_idx, layer.topk_w, layer.counts), expected[i]))
+
+
+def test_a_graph_between_other_batches(expected):
+    layer = build()
+    results(layer, inputs(6, 4096), None)                      # the largest batch comes before capturing
+    x = inputs(1, 16)
+    out = torch.empty((16, D), dtype=torch.bfloat16, device="cuda")
+    results(layer, x, None, out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dz = results(layer, x, None, out)[1]
+    for i in (2, 0, 6, 4):
+        y, _ = results(layer, inputs(i, SIZES[i]), None)
+        torch.cuda.synchronize()
+        assert (y == expected[i][0]).all()
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (out == expected[1][0]).all() and (dz == expected[1][1]).all()
+
+
+def test_helpers_leave_memory_to_their_stream():
+    from mixture_experts_layer_35_amd.layer import dequantize_mx4, quantize_mx4
+    x = torch.randn(3000, 512, device="cuda")
+    want = dequantize_mx4(*quantize_mx4(x), 512, torch.float32)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        q, s = quantize_mx4(x, side)
+        got.append(dequantize_mx4(q, s, 512, torch.float32, side))
+        del q, s
+        trample([3000 * 256, 3000 * 16])
+    torch.cuda.synchronize()
+    assert all((y == want).all() for y in got)
