@@ -68,15 +68,29 @@ def _float_type(t: torch.Tensor) -> int:
 
 
 def _row_stride(t: torch.Tensor) -> int:
-    """Elements from row to row of a matrix whose rows are contiguous (the entry points refuse rows that overlap)."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("a matrix of contiguous rows expected")
+    """Elements from row to row of a matrix whose rows are contiguous and do not overlap."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError("a matrix of contiguous rows expected, not strides %s" % (t.stride(),))
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _check(name, t, device, dtypes, shape, dense=True):
+    """The entry points take bare pointers: refuses a tensor that is not what the kernels will read or write."""
+    if t.device != device or t.dtype not in dtypes or t.shape != shape or (dense and not t.is_contiguous()):
+        raise ValueError("%s: %s%s of %s on %s expected, not %s of %s on %s" % (
+            name, "contiguous " if dense else "", list(shape), " or ".join(map(str, dtypes)), device, list(t.shape), t.dtype,
+            t.device))
+
+
+def _on_gpu(*tensors):
+    if any(not t.is_cuda or t.device != tensors[0].device for t in tensors):
+        raise ValueError("tensors on one GPU expected, not on %s" % ", ".join(str(t.device) for t in tensors))
 
 
 def quantize_mx4(x: torch.Tensor, stream=None):
     """bf16/fp32 device tensor [..., cols] whose rows are contiguous and evenly spaced -> MX4
     (codes [..., 64 R], scales [..., 4 R]), uint8, R = ceil(cols / 128)."""
+    _on_gpu(x)
     cols = x.shape[-1]
     rows = x.view(-1, cols) if x.numel() else x.reshape(0, cols)
     runs = -(-cols // 128)
@@ -89,6 +103,9 @@ def quantize_mx4(x: torch.Tensor, stream=None):
 
 def dequantize_mx4(q: torch.Tensor, s: torch.Tensor, cols: int, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """The values [..., cols] that MX4 codes and scales stand for (exact in bf16 and fp32)."""
+    _on_gpu(q, s)
+    if cols <= 0 or q.dtype != torch.uint8 or s.dtype != torch.uint8:
+        raise ValueError("uint8 codes and scales of rows of at least one value expected")
     runs = -(-cols // 128)
     if q.shape[-1] != 64 * runs or s.shape != q.shape[:-1] + (4 * runs,) or not (q.is_contiguous() and s.is_contiguous()):
         raise ValueError("codes [..., %d] and scales [..., %d], contiguous, expected" % (64 * runs, 4 * runs))
@@ -226,18 +243,19 @@ class Mx4Experts:
     capturing."""
 
     def __init__(self, w_gate, w_up, w_down, topk, n_shared=0, stream=None, **rule):
+        _on_gpu(w_gate, w_up, w_down)
         n, self.inter, self.d = w_gate.shape
         if w_up.shape != w_gate.shape or w_down.shape != (n, self.d, self.inter) or not 0 <= n_shared < n:
             raise ValueError("w_gate and w_up [n][inter][d], w_down [n][d][inter] expected, and fewer shared experts than n")
         self.n_routed, self.n_shared, self.topk, self.rule = n - n_shared, n_shared, topk, rule
         w = [quantize_mx4(x, stream) for x in (w_gate, w_up, w_down)]
         self.codes, self.scales = [q for q, _ in w], [s for _, s in w]
+        self.device = w_gate.device
         self._T, self._capacity, self._held = -1, 0, None
         self._streams = {_raw(stream)}     # those that own the weights and buffers or were recorded on them
 
     def _gate_rule(self, logits):
-        if logits.shape != (self._T, self.n_routed):
-            raise ValueError("logits [%d][%d] expected" % (self._T, self.n_routed))
+        _check("logits", logits, self.device, (torch.float32, torch.bfloat16), (self._T, self.n_routed), dense=False)
         return make_gate_rule(self._T, self.n_routed, self.topk,
                               logits="bf16" if _float_type(logits) == MOE_BF16 else "fp32", **self.rule)
 
@@ -251,7 +269,7 @@ class Mx4Experts:
     def _buffers(self, T, stream):
         """Buffers for T tokens on `stream`."""
         K, Nr, Ns, runs = self.topk, self.n_routed, self.n_shared, -(-self.d // 128)
-        device = self.codes[0].device
+        device = self.device
         self._use(stream)
         if T > self._capacity:
             # the old ones are released before the larger ones are taken
@@ -291,19 +309,26 @@ class Mx4Experts:
                 scores: torch.Tensor = None, stream=None) -> torch.Tensor:
         """u [T][d] bf16, logits [T][n_routed] fp32 or bf16 (rows of either may be padded); the choice stays in
         topk_idx, topk_w and counts.  bias [n_routed] fp32; out [T][d] bf16 and scores [T][n_routed] fp32 contiguous."""
-        T = u.shape[0]
-        if u.dtype != torch.bfloat16 or u.shape[1:] != (self.d,):
-            raise ValueError("u [T][%d] bf16 expected" % self.d)
+        T, fp32 = u.shape[0], (torch.float32,)
+        _check("u", u, self.device, (torch.bfloat16,), (T, self.d), dense=False)
+        _check("logits", logits, self.device, (torch.float32, torch.bfloat16), (T, self.n_routed), dense=False)
+        if bias is not None:
+            _check("bias", bias, self.device, fp32, (self.n_routed,))
+        if scores is not None:
+            _check("scores", scores, self.device, fp32, (T, self.n_routed))
+        if out is not None:
+            _check("out", out, self.device, (torch.bfloat16,), (T, self.d))
+        u_ld, logits_ld = _row_stride(u), _row_stride(logits)
         if out is None:
-            with _on(stream, u.device):
-                out = torch.empty((T, self.d), dtype=u.dtype, device=u.device)
+            with _on(stream, self.device):
+                out = torch.empty((T, self.d), dtype=u.dtype, device=self.device)
         if T == 0:
             return out
         self._buffers(T, stream)
-        moe_gate(self._gate_rule(logits), logits, _row_stride(logits), bias, scores, self.topk_idx, self.topk_w, stream)
+        moe_gate(self._gate_rule(logits), logits, logits_ld, bias, scores, self.topk_idx, self.topk_w, stream)
         moe_permute(self._shape, self.topk_idx, None, self.counts, self._offsets, self._tokens, self._inv, None, None,
                     self._pws, stream)
-        moe_quantize_mx4(T, self.d, MOE_BF16, u, _row_stride(u), self._xq, self._xs, stream)
+        moe_quantize_mx4(T, self.d, MOE_BF16, u, u_ld, self._xq, self._xs, stream)
         moe_grouped_ffn_mx4(self.n_routed + self.n_shared, self._offsets, T * (self.topk + self.n_shared), self._tokens,
                             self.d, self.inter, self._xq, self._xs, self.codes, self.scales, self._y, self._ws, stream)
         shared = self._y[T * self.topk:] if self.n_shared else None
@@ -312,11 +337,18 @@ class Mx4Experts:
 
     def gate_gradient(self, logits: torch.Tensor, dtopk_w: torch.Tensor, dscores: torch.Tensor = None,
                       stream=None) -> torch.Tensor:
-        """dL/dlogits of the most recent forward's choice, from dL/dtopk_w and (optional) dL/dscores."""
+        """dL/dlogits of the most recent forward's choice, from dL/dtopk_w [T][topk] and (optional) dL/dscores
+        [T][n_routed], fp32 of any strides (what is not contiguous, as an expanded mean's gradient, is copied)."""
         rule = self._gate_rule(logits)
+        _check("dtopk_w", dtopk_w, self.device, (torch.float32,), (self._T, self.topk), dense=False)
+        if dscores is not None:
+            _check("dscores", dscores, self.device, (torch.float32,), (self._T, self.n_routed), dense=False)
+        ld = _row_stride(logits)
         self._use(stream)
-        with _on(stream, logits.device):
-            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        moe_gate_backward(rule, logits, _row_stride(logits), self.topk_idx, self.topk_w, dtopk_w, dscores, dlogits,
+        with _on(stream, self.device):
+            dtopk_w = dtopk_w.contiguous()
+            dscores = None if dscores is None else dscores.contiguous()
+            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=self.device)
+        moe_gate_backward(rule, logits, ld, self.topk_idx, self.topk_w, dtopk_w, dscores, dlogits,
                           self.n_routed, stream)
         return dlogits
