@@ -271,7 +271,7 @@ class Mx4Experts:
         K, Nr, Ns, runs = self.topk, self.n_routed, self.n_shared, -(-self.d // 128)
         device = self.device
         self._use(stream)
-        if T > self._capacity:
+        if T > self._capacity or self._held is None:
             # the old ones are released before the larger ones are taken
             self._T, self._capacity, self._held = -1, 0, None
             self.topk_idx = self.topk_w = self.counts = self._offsets = self._tokens = self._inv = None
@@ -295,7 +295,7 @@ class Mx4Experts:
             self.topk_idx, self.topk_w, self.counts, self._offsets = idx[:T], w[:T], counts, offsets
             self._tokens, self._inv, self._xq, self._xs = tokens[:rows], inv[:T * K], xq[:T], xs[:T]
             self._y, self._ws, self._pws = y[:rows], ws, pws
-        if Ns:
+        if Ns and T:
             # the shared experts' rows follow the routed ones'; a graph writes their bounds and tokens itself, since other
             # batches may come between its replays
             with _on(stream, device):
@@ -322,9 +322,11 @@ class Mx4Experts:
         if out is None:
             with _on(stream, self.device):
                 out = torch.empty((T, self.d), dtype=u.dtype, device=self.device)
-        if T == 0:
-            return out
         self._buffers(T, stream)
+        if T == 0:
+            with _on(stream, self.device):
+                self.counts.zero_()
+            return out
         moe_gate(self._gate_rule(logits), logits, logits_ld, bias, scores, self.topk_idx, self.topk_w, stream)
         moe_permute(self._shape, self.topk_idx, None, self.counts, self._offsets, self._tokens, self._inv, None, None,
                     self._pws, stream)
