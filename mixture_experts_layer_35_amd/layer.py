@@ -239,8 +239,8 @@ class Mx4Experts:
 
     Buffers hold the largest batch so far and are shared by all calls: calls on different streams have to be ordered by
     the caller, as for every workspace, and topk_idx, topk_w and counts hold the last call's choice.  A call's results
-    belong to its stream.  A graph that captures a call keeps the buffers' addresses: run the largest batch before
-    capturing."""
+    belong to its stream.  A captured call uses the buffers of its time, which the layer keeps from then on: running the
+    largest batch before capturing keeps one set."""
 
     def __init__(self, w_gate, w_up, w_down, topk, n_shared=0, stream=None, **rule):
         _on_gpu(w_gate, w_up, w_down)
@@ -251,7 +251,7 @@ class Mx4Experts:
         w = [quantize_mx4(x, stream) for x in (w_gate, w_up, w_down)]
         self.codes, self.scales = [q for q, _ in w], [s for _, s in w]
         self.device = w_gate.device
-        self._T, self._capacity, self._held = -1, 0, None
+        self._T, self._capacity, self._held, self._captured, self._kept = -1, 0, None, False, []
         self._streams = {_raw(stream)}     # those that own the weights and buffers or were recorded on them
 
     def _gate_rule(self, logits):
@@ -262,7 +262,7 @@ class Mx4Experts:
     def _use(self, stream):
         """Before work on `stream`: weights and buffers that are dropped later are not reused before it has ended."""
         if _raw(stream) not in self._streams:
-            for t in self.codes + self.scales + list(self._held or ()):
+            for t in self.codes + self.scales + [t for held in self._kept + [self._held or ()] for t in held]:
                 t.record_stream(_torch_stream(stream, t.device))
             self._streams.add(_raw(stream))
 
@@ -272,7 +272,9 @@ class Mx4Experts:
         device = self.device
         self._use(stream)
         if T > self._capacity or self._held is None:
-            # the old ones are released before the larger ones are taken
+            # the old ones are released before the larger ones are taken, unless a graph may hold their addresses
+            if self._captured:
+                self._kept.append(self._held)
             self._T, self._capacity, self._held = -1, 0, None
             self.topk_idx = self.topk_w = self.counts = self._offsets = self._tokens = self._inv = None
             self._xq = self._xs = self._y = self._ws = self._pws = None
@@ -295,11 +297,13 @@ class Mx4Experts:
             self.topk_idx, self.topk_w, self.counts, self._offsets = idx[:T], w[:T], counts, offsets
             self._tokens, self._inv, self._xq, self._xs = tokens[:rows], inv[:T * K], xq[:T], xs[:T]
             self._y, self._ws, self._pws = y[:rows], ws, pws
+        with _on(stream, device):
+            self._captured = self._captured or torch.cuda.is_current_stream_capturing()
         if Ns and T:
-            # the shared experts' rows follow the routed ones'; a graph writes their bounds and tokens itself, since other
-            # batches may come between its replays
+            # the shared experts' rows follow the routed ones'.  Their bounds and tokens stay from one batch to the next of
+            # its size; once a call has been captured every call writes them, as replays may come between any two
             with _on(stream, device):
-                if T != self._T or torch.cuda.is_current_stream_capturing():
+                if T != self._T or self._captured:
                     torch.arange(T * K, T * (K + Ns) + 1, T, out=self._offsets[Nr:])
                     for j in range(Ns):
                         torch.arange(T, out=self._tokens[T * (K + j):T * (K + j + 1)])

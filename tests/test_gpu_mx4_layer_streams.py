@@ -115,3 +115,40 @@ def test_helpers_leave_memory_to_their_stream():
         trample([3000 * 256, 3000 * 16])
     torch.cuda.synchronize()
     assert all((y == want).all() for y in got)
+
+
+@pytest.mark.parametrize("replays", [0, 1])
+def test_batches_of_one_size_around_a_graph_of_another(expected, replays):
+    layer, x = build(), inputs(1, 16)
+    results(layer, inputs(6, 4096), None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, dz = results(layer, x, None)
+    for i in (1, 6, 6, 1, 1):                                  # the captured size too, before its first replay
+        got = results(layer, inputs(i, SIZES[i]), None)
+        torch.cuda.synchronize()
+        assert all((a == b).all() for a, b in zip(got, expected[i]))
+        for _ in range(replays):
+            y.zero_()
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert (y == expected[1][0]).all() and (dz == expected[1][1]).all()
+
+
+def test_a_graph_before_a_larger_batch(expected):
+    layer, x = build(), inputs(1, 16)
+    results(layer, x, None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, dz = results(layer, x, None)
+    for i in (2, 6):
+        got = results(layer, inputs(i, SIZES[i]), None)
+        trample([4 * 16 * K, 4 * NR, 16 * D, 2 * 16 * (K + NS) * D, 4 * 16 * (K + NS)])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all((a == b).all() for a, b in zip(got, expected[i]))
+        assert (y == expected[1][0]).all() and (dz == expected[1][1]).all()
