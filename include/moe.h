@@ -460,6 +460,9 @@ int moe_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t *q, const uint8
  * Deterministic: no sum's order changes from call to call.  max_rows, n_exp, d and
  * inter choose it, so a row among more rows can differ in the last bit of a sum
  * (and, where that meets a rounding boundary, by a code of h).
+ * Infinities and NaN go where the formula takes them: a block of scale 255 (NaN) of a row of x makes its y[r]
+ * NaN, one of a gate or up row of expert e (or an H that is infinite or NaN) every y[r] whose H it meets, one of
+ * a row of W_down[e] that feature of expert e's rows; nothing else changes.
  * n_exp <= 1024 experts; offsets [n_exp+1] int32 on the device, offsets[0] = 0,
  * non-decreasing, offsets[n_exp] <= max_rows.  d and inter are any positive
  * sizes (rows padded to whole runs as above).
