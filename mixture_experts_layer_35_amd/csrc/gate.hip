@@ -8,6 +8,7 @@
 
 #include "common.h"
 #include "internal.h"
+#include "variants.h"
 
 // A product and a sum that the definition rounds one after the other stay two roundings.
 #pragma clang fp contract(off)
@@ -602,32 +603,26 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(const GateA
     if (live) store_row<DT, L, V, true>((char *)a.dlogits + t * a.dld * (DT == DT_F32 ? 4 : 2), l, E, a.dvec, o);
 }
 
-// f(L, V) for a token width that holds E experts.  Up to 16 values a lane keep a wave on four tokens
-// at 256 experts, which costs the fewest instructions a token; a batch whose waves would leave compute
-// units idle takes four values a lane instead, the shortest chain of instructions to its end.  256 experts:
-// 16384 tokens 12.7 us with 16 values a lane, 17.2 with four; one token 7.6 us and 5.4.
+// f(L, V) for the token's width.
 template <class F>
 hipError_t with_width(int64_t T, int E, F f) {
+    const GateWidth w = gate_width(T, E, device_cus());
+    hipError_t e = hipErrorInvalidValue;
+    auto width = [&](auto l, auto v) {
+        if (w.lanes == decltype(l)::value && w.values == decltype(v)::value) e = f(l, v);
+    };
     using std::integral_constant;
-    const bool few = T * ((E + 3) / 4) <= (int64_t)device_cus() * 4 * 64;   // lanes of 4 values fill one wave a SIMD
-    if (E <= 32) return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
-    if (E <= 64) {
-        if (few) return f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
-        return f(integral_constant<int, 8>{}, integral_constant<int, 8>{});
-    }
-    if (E <= 128) {
-        if (few) return f(integral_constant<int, 32>{}, integral_constant<int, 4>{});
-        return f(integral_constant<int, 16>{}, integral_constant<int, 8>{});
-    }
-    if (E <= 256) {
-        if (few) return f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
-        return f(integral_constant<int, 16>{}, integral_constant<int, 16>{});
-    }
-    if (E <= 512) {
-        if (few) return f(integral_constant<int, 64>{}, integral_constant<int, 8>{});
-        return f(integral_constant<int, 32>{}, integral_constant<int, 16>{});
-    }
-    return f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
+    width(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+    width(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+    width(integral_constant<int, 32>{}, integral_constant<int, 4>{});
+    width(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+    width(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    width(integral_constant<int, 16>{}, integral_constant<int, 8>{});
+    width(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+    width(integral_constant<int, 16>{}, integral_constant<int, 16>{});
+    width(integral_constant<int, 32>{}, integral_constant<int, 16>{});
+    width(integral_constant<int, 64>{}, integral_constant<int, 16>{});
+    return e;
 }
 
 // A launch holds fewer than 2^32 threads: f(first token, grid) for parts of the batch of TPB tokens a workgroup.

@@ -7,6 +7,7 @@
 #include "common.h"
 #include "internal.h"
 #include "lds_ring.h"
+#include "variants.h"
 
 namespace moe {
 
@@ -447,7 +448,7 @@ constexpr int kMx4EndBytes = kMaxExperts * 4;
 // waves of a workgroup share a tile, each a quarter of the segments, and add up in LDS, in the order of the waves,
 // which leaves room for 16 tokens.  One token, 8 experts of 7168 x 2048: gate/up 25 us, down 14 us (187 MB of
 // weights at 4.8 TB/s).
-constexpr int mx4_stream_tokens(bool split) { return split ? 16 : 32; }
+constexpr int mx4_stream_tokens(bool split) { return mx4_tokens(split ? kMx4Shared : kMx4Stream); }
 constexpr int mx4_slot_bytes(bool split) { return kMx4WeightBytes + mx4_stream_tokens(split) * 128; }
 constexpr int kMx4ScaleSlot = (64 + 32) * 16;            // of two segments (WIDE); three of 8 bytes a row fit as well
 constexpr int kMx4PartBytes = (kMx4Waves - 1) * 8 * 64 * 16;
@@ -912,33 +913,18 @@ hipError_t launch_mx4_ffn(const Mx4Ffn &a, hipStream_t s) {
     down.yvec = (uintptr_t)a.y % 16 == 0 && a.d % 8 == 0;
     const int64_t cus = device_cus();
     const unsigned grid = (unsigned)((cus + 7) / 8 * 8);
-    const int64_t experts = a.max_rows < a.n_exp ? a.max_rows : a.n_exp;
-    // row blocks of bm rows, at most
-    auto blocks = [&](int64_t bm) { return experts + (a.max_rows - experts) / bm; };
     auto pass = [&](auto gateup, auto wide, const Mx4Pass &p, int64_t ftiles) {
         constexpr bool GU = decltype(gateup)::value, W = decltype(wide)::value;
-        // Four waves share a tile where that ends sooner: `rounds` tiles a workgroup, one after the other, each a
-        // quarter of the segments and, for adding up, as long as 2.5 more, against all segments by one wave.  With
-        // rows of 7168 (28 segments) and 2048 (8), experts of 7168 x 2048: 1 token to 8 experts, gate/up in 2 rounds
-        // shared 42 us (the whole call), not shared 50; 32 tokens of one expert, down in 1 round 23 against 26,
-        // 48 tokens in 2 rounds 28 against 26.
-        const int64_t segs = (p.kruns + 1) / 2, rounds = (blocks(mx4_stream_tokens(true)) * ftiles + cus - 1) / cus;
-        if (rounds * (segs + 10) < 4 * segs)
-            return mx4_launch<mx4_stream_kernel<GU, true, W>>(grid, kMx4Threads, mx4_stream_lds(true), p, s);
-        // Tiles for a wave by itself as long as there is no more than one for each wave: one expert of 7168 x 2048,
-        // 384 tokens, gate/up of 768 tiles 42 us (the whole call) against 52 in the tile kernel, 640 tokens, 1280 tiles
-        // 65 against 53; 8 x 512 tokens of 512 x 256, 1024 tiles in either pass 16 against 22.
-        if (blocks(mx4_stream_tokens(false)) * ftiles <= cus * kMx4Waves)
-            return mx4_launch<mx4_stream_kernel<GU, false, W>>(grid, kMx4Threads, mx4_stream_lds(false), p, s);
-        // Tiles of up to 160 tokens where experts of the average size need fewer of them than of 128 (an eighth is
-        // left for experts above the average) and there is one for each workgroup.  256 experts of 7168 x 2048:
-        // 90 rows 1290 us either way, 128 rows 1410 us against 1540 with 128 tokens, 219 rows 2430 against 2100,
-        // 256 rows 2330 against 2430; 8 experts of 2048 x 1024, 128 rows, 64 tiles: 33 against 30.
-        const int64_t n = a.n_exp;
-        const bool fewer = (a.max_rows + 140 * n - 1) / (140 * n) < (a.max_rows + 112 * n - 1) / (112 * n);
-        if (fewer && blocks(160) * ((ftiles + 3) / 4) >= cus)
-            return mx4_launch<mx4_tile_kernel<GU, W, 5>>(grid, kMx4TileThreads, mx4_tile_lds(5), p, s);
-        return mx4_launch<mx4_tile_kernel<GU, W, 4>>(grid, kMx4TileThreads, mx4_tile_lds(4), p, s);
+        switch (mx4_variant(a.max_rows, a.n_exp, p.kruns, ftiles, cus)) {
+            case kMx4Shared:
+                return mx4_launch<mx4_stream_kernel<GU, true, W>>(grid, kMx4Threads, mx4_stream_lds(true), p, s);
+            case kMx4Stream:
+                return mx4_launch<mx4_stream_kernel<GU, false, W>>(grid, kMx4Threads, mx4_stream_lds(false), p, s);
+            case kMx4Tile160:
+                return mx4_launch<mx4_tile_kernel<GU, W, 5>>(grid, kMx4TileThreads, mx4_tile_lds(5), p, s);
+            default:
+                return mx4_launch<mx4_tile_kernel<GU, W, 4>>(grid, kMx4TileThreads, mx4_tile_lds(4), p, s);
+        }
     };
     auto either = [&](auto gateup, const Mx4Pass &p, int64_t tiles) {
         const uintptr_t all = (uintptr_t)p.xs | (uintptr_t)p.s0 | (uintptr_t)p.s1;
