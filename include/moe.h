@@ -410,7 +410,8 @@ int moe_gate(const moe_gate_rule *rule, const void *logits, int64_t ld, const fl
  * logits, ld, topk_idx, topk_w as given to and by moe_gate (indices distinct
  * within a token); dtopk_w [T][K] fp32; dscores [T][n_experts] fp32 or NULL;
  * dlogits [T] rows of n_experts values in logits_dtype, dld elements apart,
- * every one of which is written.  Sums run in fp32 in a fixed order.
+ * every one of which is written.  Sums run in fp32, in an order that T and n_experts
+ * choose; none changes from call to call.
  */
 int moe_gate_backward(const moe_gate_rule *rule, const void *logits, int64_t ld, const int32_t *topk_idx,
                       const float *topk_w, const float *dtopk_w, const float *dscores, void *dlogits, int64_t dld,
@@ -443,7 +444,9 @@ int moe_quantize_mx4(int64_t rows, int32_t cols, int32_t x_dtype, const void *x,
 
 /*
  * moe_dequantize_mx4 -- the values of codes q and scales s as y_dtype (MOE_F32 or
- * MOE_BF16), rows ld elements apart.  Exact in both types (s = 255 gives NaN).
+ * MOE_BF16), rows ld elements apart.  Exact in both types; s = 255 gives NaN, and
+ * values past the largest number infinity (magnitudes 4 and 6 at s = 253, 2 and up at
+ * 254; moe_quantize_mx4 gives no scale above 252 but 255).
  * quantise + dequantise is the rounding of training with MX4 weights: the bf16
  * values go through moe_forward and moe_backward, whose weight gradients are
  * then those of the unrounded weights by the straight-through rule.
@@ -457,9 +460,10 @@ int moe_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t *q, const uint8
  * for the rows r in [offsets[e], offsets[e+1]) of expert e, x_r = x[gather[r]]
  * (gather NULL: x[r]); Q is moe_quantize_mx4's rounding of the fp32 values;
  * products of codes and scales are summed in fp32; y [max_rows][d] is bf16.
- * Deterministic: no sum's order changes from call to call.  max_rows, n_exp, d and
- * inter choose it, so a row among more rows can differ in the last bit of a sum
- * (and, where that meets a rounding boundary, by a code of h).
+ * Deterministic: no sum's order changes from call to call.  max_rows, n_exp, d, inter,
+ * the card's compute units and whether the scales lie at multiples of 16 bytes choose
+ * it, so a row among more rows can differ in the last bit of a sum (and, where
+ * that meets a rounding boundary, by a code of h).
  * Infinities and NaN go where the formula takes them: a block of scale 255 (NaN) of a row of x makes its y[r]
  * NaN, one of a gate or up row of expert e (or an H that is infinite or NaN) every y[r] whose H it meets, one of
  * a row of W_down[e] that feature of expert e's rows; nothing else changes.

@@ -115,7 +115,8 @@ __device__ __forceinline__ float softmax_exp(float z, float m) {
 
 // sigmoid_score of V logits, the same bits.  With r within one ulp of 1/d, r + r (1 - d r) is 1/d
 // correctly rounded (Markstein); tried against the division at every float d >= 1 it fails only above
-// 2^126, where r itself is no normal number.  A third of the division's instructions.
+// 2^126, where r itself is no normal number.  A third of the division's instructions, where all lanes of the wave have
+// logits above -87: experts out of use, and lanes' places past E, count as -infinity and take the division.
 template <int V>
 __device__ __forceinline__ void sigmoid_scores(const float (&z)[V], float (&s)[V]) {
     float top = 0.0f;
