@@ -488,11 +488,12 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs a) {
 
 __host__ __device__ inline int gate_backward_lds_words(int E) { return (E + 3) & ~3; }
 
-// With D the sum of the chosen scores and p_j = s_j / D, w_j = c p_j gives dL/ds_j = c (g_j - sum_i g_i p_i) / D, without
+// With D the sum of the chosen scores, w_j = c s_j / D gives dL/ds_j = c (g_j - sum_i g_i s_i / D) / D, without
 // renormalisation c g_j; the scores' own gradient is added to that, and
 // dL/dz = ds s (1 - s) for sigmoid scores, s (ds - sum_e ds_e s_e) for softmax ones.
-// Only products s ds are formed: c p_j (g_j - sum_i g_i p_i) is of the order of g for any D, where 1 / D and ds overflow
-// for chosen scores near the smallest floats.
+// Near the smallest floats 1 / D and ds overflow, though s ds is of the order of g for any D.  There (D < 2^-64) the chosen
+// scores are taken 2^100 times as large, which is exact, so that ds comes out 2^100 times smaller, and s ds is formed from
+// the two before anything is added.
 //
 // Every row of dlogits is written whole, zeros included.  16384 tokens, 8 of 256, sigmoid, fp32: 5 us for 19 MB, mostly
 // those zeros.  65521 tokens of 64 experts, softmax and a gradient at every score, bf16: 9 us for 38 MB.
@@ -506,7 +507,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(const GateA
     extern __shared__ __align__(16) uint32_t lds[];
     const int sub = threadIdx.x / L, l = threadIdx.x % L;
     const int E = a.E, K = a.K;
-    float *dsl = (float *)(lds + sub * gate_backward_lds_words(E));   // the slots' part of s ds, or of dz
+    float *dsl = (float *)(lds + sub * gate_backward_lds_words(E));   // the slots' part of ds, of s ds, or of dz
     const int64_t t0 = a.t0 + (int64_t)blockIdx.x * TPB + sub;
     const bool live = t0 < a.T;
     const int64_t t = live ? t0 : a.T - 1;
@@ -548,7 +549,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(const GateA
             sigmoid_scores<V>(z, s);
         }
     }
-    // Slots: s_j, then s_j / D, and g_j.  The weights' sum is fixed under renormalisation, so a common part of the g
+    // Slots: s_j and g_j.  The weights' sum is fixed under renormalisation, so a common part of the g
     // moves nothing: taking g_0 away first keeps the difference below exact where the g are alike
     // (K = 1 gives 0).
     const float g0 = a.renorm && w0 != 0.0f ? dw0 : 0.0f;
@@ -560,24 +561,22 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(const GateA
         gj[q] = on ? gj[q] - g0 : 0.0f;
         sum_s += sj[q];
     }
-    float pj[Q], mean = 0.0f;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) pj[q] = sj[q];
+    float invd = 1.0f, mean = 0.0f, up = 1.0f;
     if (a.renorm) {
         const float D = lanes_sum<L>(sum_s);
+        up = D < 0x1p-64f ? 0x1p100f : 1.0f;
+        invd = D > 0.0f ? 1.0f / (D * up) : 0.0f;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            pj[q] = D > 0.0f ? sj[q] / D : 0.0f;
-            mean += gj[q] * pj[q];
-        }
-        mean = lanes_sum<L>(mean);
+        for (int q = 0; q < Q; ++q) mean += gj[q] * (sj[q] * up);
+        mean = lanes_sum<L>(mean) * invd;
     }
+    const bool tiny = up != 1.0f;
     token_lds_order();
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         if (ij[q] < 0) continue;
-        const float sds = (gj[q] - mean) * pj[q] * a.scale;
-        dsl[ij[q]] = DENSE ? sds : sds * (1.0f - sj[q]);
+        const float ds = (gj[q] - mean) * invd * a.scale, sds = ds * (sj[q] * up);
+        dsl[ij[q]] = !DENSE ? sds * (1.0f - sj[q]) : tiny ? sds : ds;
     }
     token_lds_order();
 
@@ -591,15 +590,30 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(const GateA
     }
     if (DENSE) {
         float dot = 0.0f;
+        // an expert out of use takes no gradient, whatever the caller's dscores holds there
+        if (__any(tiny)) {
+            float sds[V];
 #pragma unroll
-        for (int r = 0; r < V; ++r) {
-            // an expert out of use takes no gradient, whatever the caller's dscores holds there
-            o[r] = in_use(z[r]) ? (a.ds ? d[r] * s[r] + o[r] : o[r]) : 0.0f;
-            dot += o[r];
+            for (int r = 0; r < V; ++r) {
+                const float own = a.ds && in_use(z[r]) ? d[r] : 0.0f;
+                o[r] = !in_use(z[r]) ? 0.0f : tiny ? o[r] : o[r] + own;
+                sds[r] = tiny ? own * s[r] + o[r] : o[r] * s[r];
+                dot += sds[r];
+            }
+            if (a.softmax) dot = lanes_sum<L>(dot);
+#pragma unroll
+            for (int r = 0; r < V; ++r)
+                o[r] = !a.softmax ? sds[r] * (1.0f - s[r]) : tiny ? sds[r] - s[r] * dot : s[r] * (o[r] - dot);
+        } else {
+#pragma unroll
+            for (int r = 0; r < V; ++r) {
+                o[r] = in_use(z[r]) ? (a.ds ? d[r] + o[r] : o[r]) : 0.0f;
+                dot += o[r] * s[r];
+            }
+            if (a.softmax) dot = lanes_sum<L>(dot);
+#pragma unroll
+            for (int r = 0; r < V; ++r) o[r] = a.softmax ? s[r] * (o[r] - dot) : o[r] * s[r] * (1.0f - s[r]);
         }
-        if (a.softmax) dot = lanes_sum<L>(dot);
-#pragma unroll
-        for (int r = 0; r < V; ++r) o[r] = a.softmax ? o[r] - s[r] * dot : o[r] * (1.0f - s[r]);
     }
     if (live) store_row<DT, L, V, true>((char *)a.dlogits + t * a.dld * (DT == DT_F32 ? 4 : 2), l, E, a.dvec, o);
 }
