@@ -262,8 +262,9 @@ __device__ __forceinline__ void lanes_top2(uint32_t &k1, uint32_t &k2, int width
 // over the token's lanes, and the slots' weights, over their sum where that is asked for.  Nothing but the logits is
 // read and nothing but the outputs written.
 //
-// 16384 tokens, 8 of 256 experts, 4 of 8 groups, fp32: 12.7 us for 17.9 MB, bound by vector instructions (four tokens
-// a wave, four waves a SIMD).  65521 tokens, 6 of 64 by softmax, bf16: 10 us for 11.5 MB.  One token: 4.2 us, the
+// 16384 tokens, 8 of 256 experts, 4 of 8 groups, fp32: 12.8 us for 17.9 MB, bound by vector instructions (four tokens
+// a wave, four waves a SIMD): of 1183 a wave the 8 rounds take some 400, the exponentials 260, the groups 180, the keys
+// 100, the reciprocals 50.  65521 tokens, 6 of 64 by softmax, bf16: 11 us for 11.5 MB.  One token: 4.2 us, the
 // launch and one chain of dependent steps.
 template <int DT, int L, int V>
 __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs a) {
@@ -495,8 +496,8 @@ __host__ __device__ inline int gate_backward_lds_words(int E) { return (E + 3) &
 // scores are taken 2^100 times as large, which is exact, so that ds comes out 2^100 times smaller, and s ds is formed from
 // the two before anything is added.
 //
-// Every row of dlogits is written whole, zeros included.  16384 tokens, 8 of 256, sigmoid, fp32: 5 us for 19 MB, mostly
-// those zeros.  65521 tokens of 64 experts, softmax and a gradient at every score, bf16: 9 us for 38 MB.
+// Every row of dlogits is written whole, zeros included.  16384 tokens, 8 of 256, sigmoid, fp32: 6 us for 19 MB, mostly
+// those zeros.  65521 tokens of 64 experts, softmax and a gradient at every score, bf16: 10.7 us for 38 MB.
 //
 // DENSE: softmax scores, or a gradient at every score.  Otherwise only the chosen logits have a
 // gradient, and only they are read.

@@ -606,10 +606,13 @@ __global__ __launch_bounds__(kMx4Threads, 1) void mx4_stream_kernel(const Mx4Pas
 // and arrive in time beside weights from memory; it is for experts of about 128 rows, most of which then need
 // one tile and read their weights once.
 //
-// 256 experts of 7168 x 2048: at 4 rows each bound by the stream of weights (5.98 GB in 890 us, 6.7 TB/s), at 128 rows by
-// the stream and the products together (gate/up 910 us, down 500), neither of which the other's waits fill whole.
-// 32 experts, 512 rows: products (gate/up 350 us, 2.7 of 6.7 PFLOP/s), the loads from L2 into LDS that feed them (8 of
+// 256 experts of 7168 x 2048: at 4 rows each bound by the stream of weights (5.85 GB in 894 us, 6.5 TB/s), at 128 rows by
+// the stream and the products together (gate/up 940 us, down 490), neither of which the other's waits fill whole.
+// 32 experts, 512 rows: products (gate/up 360 us, 2.7 of 6.7 PFLOP/s), the loads from L2 into LDS that feed them (8 of
 // 16 TB/s) and the epilogue, which the multiplying waves do not overlap.
+//
+// Two waves a SIMD have 256 registers each.  Gate/up of 160 tokens takes all of them and keeps three values in
+// scratch, read back once a tile; the loading waves, which have as many, need a few dozen.
 constexpr int kMx4TileThreads = 512;
 constexpr int kMx4WeightStages = 3;
 constexpr int mx4_token_stages(int cap) { return cap <= 4 ? 3 : 2; }
