@@ -483,6 +483,70 @@ int moe_grouped_ffn_mx4(int32_t n_exp, const int32_t *offsets, int64_t max_rows,
 size_t moe_ffn_mx4_workspace_bytes(int64_t max_rows, int32_t inter);
 
 /* ------------------------------------------------------------------------ */
+/* products of experts                                                      */
+
+/*
+ * One matrix product per expert over ragged rows, for experts of any kind: expert e owns
+ * the rows r in [offsets[e], offsets[e+1]) of a batch of max_rows rows.
+ *   n_exp <= 1024 experts; offsets [n_exp+1] int32 on the device, offsets[0] = 0,
+ *   non-decreasing, offsets[n_exp] <= max_rows < 2^31 (moe_permute gives them).  Rows from
+ *   offsets[n_exp] on are neither read nor written; an expert may have none.
+ *   w [n_exp][out][in] dense; in and out any sizes up to 2^20 with in * out <= 2^29.
+ *   Rows of the other matrices are *_ld elements apart (*_ld >= the row's values); addresses
+ *   and rows at multiples of 16 bytes are the fast case, any other is taken.
+ * Products are summed in fp32 (8-bit integers in int32, exactly) and rounded once to the
+ * output's type, MOE_BF16 or MOE_F32.  Deterministic: the order of a sum depends on the sizes, the
+ * alignment and the card alone, so a row among more rows can differ in a sum's last bit.
+ * Infinities and NaN go where the formula takes them, and to no other row or feature.
+ */
+
+/*
+ * moe_grouped_product -- y[r] = W[e] x[gather[r]] (gather NULL: x[r]).
+ * x bf16 rows of in values, w bf16, y rows of out values in y_dtype.
+ */
+int moe_grouped_product(int32_t n_exp, const int32_t *offsets, int64_t max_rows, const int32_t *gather, int32_t in,
+                        int32_t out, const void *x, int64_t x_ld, const void *w, int32_t y_dtype, void *y, int64_t y_ld,
+                        void *stream);
+
+/*
+ * moe_grouped_product_dx -- its gradient at the rows of x: dx[r] = W[e]^T dy[r], a row for every row r (a
+ * token's rows are added up by moe_combine with weights of 1).
+ * dy bf16 rows of out values, w as above, dx rows of in values in dx_dtype.
+ */
+int moe_grouped_product_dx(int32_t n_exp, const int32_t *offsets, int64_t max_rows, int32_t in, int32_t out,
+                           const void *dy, int64_t dy_ld, const void *w, int32_t dx_dtype, void *dx, int64_t dx_ld,
+                           void *stream);
+
+/*
+ * moe_grouped_product_dw -- its gradient at the weights: dw[e] = sum over r of dy[r] x[gather[r]]^T, with
+ * `accumulate` (MOE_F32 only) added to what dw holds.  dw [n_exp][out][in] dense in dw_dtype, every value of
+ * which is written: 0 (or kept) for an expert without rows.
+ */
+int moe_grouped_product_dw(int32_t n_exp, const int32_t *offsets, int64_t max_rows, const int32_t *gather, int32_t in,
+                           int32_t out, const void *x, int64_t x_ld, const void *dy, int64_t dy_ld, int32_t dw_dtype,
+                           void *dw, int32_t accumulate, void *stream);
+
+/*
+ * moe_quantize_int8 -- x [rows] rows of cols values (x_dtype MOE_F32 or MOE_BF16), ld elements apart, to
+ * 8-bit integers with a scale a row: with m = max(largest magnitude of the row, 2^-100),
+ *   s = m / 127,   code = x * (127 / m) to the nearest whole number, ties to even
+ * (fp32 operations, each rounded once; codes lie in -127 .. 127).  A row with an infinity or NaN gets s = NaN and
+ * codes 0.  q [rows] rows of ceil(cols / 128) * 128 codes, zeros behind the last, 16-byte aligned; s [rows] fp32.
+ * Rows of tokens get a scale a token, rows of weights [n_exp * out] a scale an output channel.
+ */
+int moe_quantize_int8(int64_t rows, int32_t cols, int32_t x_dtype, const void *x, int64_t ld, int8_t *q, float *s,
+                      void *stream);
+
+/*
+ * moe_grouped_product_int8 -- y[r][f] = (sum over k of xq[gather[r]][k] wq[e][f][k]) * x_scales[gather[r]] *
+ * w_scales[e][f], multiplied from left to right in fp32.  x, w codes and scales of moe_quantize_int8 (w of
+ * n_exp * out rows of in values); in <= 131072, so that no sum leaves 32 bits; an expert's codes at most 2^30 bytes.
+ */
+int moe_grouped_product_int8(int32_t n_exp, const int32_t *offsets, int64_t max_rows, const int32_t *gather, int32_t in,
+                             int32_t out, const int8_t *x, const float *x_scales, const int8_t *w, const float *w_scales,
+                             int32_t y_dtype, void *y, int64_t y_ld, void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* helpers                                                                  */
 
 enum { MOE_WS_ROUTE = 0, MOE_WS_PERMUTE = 1, MOE_WS_FORWARD = 2 };

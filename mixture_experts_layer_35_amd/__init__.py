@@ -37,7 +37,8 @@ EXPORTED = ("moe_route", "moe_permute", "moe_grouped_ffn", "moe_combine", "moe_f
             "moe_transpose_expert_weights", "moe_backward", "moe_backward_timed", "moe_backward_workspace_bytes",
             "moe_quantize_1x128", "moe_quantize_weights_128x128", "moe_quantize_128x1", "moe_gate",
             "moe_gate_backward", "moe_quantize_mx4", "moe_dequantize_mx4", "moe_grouped_ffn_mx4",
-            "moe_ffn_mx4_workspace_bytes", "moe_last_error", "moe_version")
+            "moe_ffn_mx4_workspace_bytes", "moe_grouped_product", "moe_grouped_product_dx", "moe_grouped_product_dw",
+            "moe_quantize_int8", "moe_grouped_product_int8", "moe_last_error", "moe_version")
 
 
 class MoeError(RuntimeError):
@@ -124,6 +125,11 @@ def lib():
                 "moe_quantize_mx4": [i64, i32, i32, P, i64, P, P, P],
                 "moe_dequantize_mx4": [i64, i32, P, P, i32, P, i64, P],
                 "moe_grouped_ffn_mx4": [i32, P, i64, P, i32, i32, P, P, P, P, P, P, sz, P],
+                "moe_grouped_product": [i32, P, i64, P, i32, i32, P, i64, P, i32, P, i64, P],
+                "moe_grouped_product_dx": [i32, P, i64, i32, i32, P, i64, P, i32, P, i64, P],
+                "moe_grouped_product_dw": [i32, P, i64, P, i32, i32, P, i64, P, i64, i32, P, i32, P],
+                "moe_quantize_int8": [i64, i32, i32, P, i64, P, P, P],
+                "moe_grouped_product_int8": [i32, P, i64, P, i32, i32, P, P, P, P, i32, P, i64, P],
             }
             for name, args in sig.items():
                 f = getattr(L, name)
@@ -392,3 +398,30 @@ def moe_grouped_ffn_mx4(n_exp, offsets, max_rows, gather, d, inter, x, x_scales,
     return _check(lib().moe_grouped_ffn_mx4(n_exp, _ptr(offsets), max_rows, _ptr(gather), d, inter, _ptr(x),
                                             _ptr(x_scales), wa[0] if wa else None, sa[0] if sa else None, _ptr(y),
                                             _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_grouped_product(n_exp, offsets, max_rows, gather, in_, out, x, x_ld, w, y_dtype, y, y_ld, stream=None):
+    return _check(lib().moe_grouped_product(n_exp, _ptr(offsets), max_rows, _ptr(gather), in_, out, _ptr(x), x_ld,
+                                            _ptr(w), y_dtype, _ptr(y), y_ld, _stream(stream)))
+
+
+def moe_grouped_product_dx(n_exp, offsets, max_rows, in_, out, dy, dy_ld, w, dx_dtype, dx, dx_ld, stream=None):
+    return _check(lib().moe_grouped_product_dx(n_exp, _ptr(offsets), max_rows, in_, out, _ptr(dy), dy_ld, _ptr(w),
+                                               dx_dtype, _ptr(dx), dx_ld, _stream(stream)))
+
+
+def moe_grouped_product_dw(n_exp, offsets, max_rows, gather, in_, out, x, x_ld, dy, dy_ld, dw_dtype, dw, accumulate,
+                           stream=None):
+    return _check(lib().moe_grouped_product_dw(n_exp, _ptr(offsets), max_rows, _ptr(gather), in_, out, _ptr(x), x_ld,
+                                               _ptr(dy), dy_ld, dw_dtype, _ptr(dw), int(accumulate), _stream(stream)))
+
+
+def moe_quantize_int8(rows, cols, x_dtype, x, ld, q, s, stream=None):
+    return _check(lib().moe_quantize_int8(rows, cols, x_dtype, _ptr(x), ld, _ptr(q), _ptr(s), _stream(stream)))
+
+
+def moe_grouped_product_int8(n_exp, offsets, max_rows, gather, in_, out, x, x_scales, w, w_scales, y_dtype, y, y_ld,
+                             stream=None):
+    return _check(lib().moe_grouped_product_int8(n_exp, _ptr(offsets), max_rows, _ptr(gather), in_, out, _ptr(x),
+                                                 _ptr(x_scales), _ptr(w), _ptr(w_scales), y_dtype, _ptr(y), y_ld,
+                                                 _stream(stream)))

@@ -1274,3 +1274,219 @@ int moe_grouped_ffn_mx4(int32_t n_exp, const int32_t *offsets, int64_t max_rows,
 }
 
 }  // extern "C"
+
+// ---- products of experts ------------------------------------------------------
+
+namespace {
+
+// What the grouped products share.  A matrix and a tile's rows are addressed in 32 bits, tiles counted in 32 bits.
+int check_product(int32_t n_exp, int64_t max_rows, int32_t in, int32_t out, const char *fn) {
+    if (n_exp <= 0 || in <= 0 || out <= 0 || max_rows < 0)
+        return fail(MOE_ERR_INVALID_ARG, "%s: sizes must be positive (max_rows >= 0)", fn);
+    if (n_exp > kMaxExperts) return fail(MOE_ERR_UNSUPPORTED, "%s: n_exp = %d exceeds %d", fn, n_exp, kMaxExperts);
+    const int64_t wide = in > out ? in : out;
+    if (max_rows >= (1ll << 31) || wide > (1 << 20) || (int64_t)in * out > (1ll << 29) ||
+        (max_rows / 16 + n_exp) * (wide / 64 + 1) >= (1ll << 31))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: max_rows = %lld, in = %d, out = %d are too large for one call", fn,
+                    (long long)max_rows, in, out);
+    return MOE_OK;
+}
+
+int check_rows(int64_t ld, int32_t cols, const char *name, const char *fn) {
+    if (ld < cols || ld >= (1ll << 40))
+        return fail(MOE_ERR_INVALID_ARG, "%s: %s_ld = %lld for rows of %d values", fn, name, (long long)ld, cols);
+    return MOE_OK;
+}
+
+int check_out(int32_t dtype, const char *fn) {
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: output dtype %d", fn, dtype);
+    return MOE_OK;
+}
+
+// Rows of `out` that take 16-byte stores.
+int wide_rows(const void *out, int64_t ld, int32_t cols, int32_t dtype) {
+    const int n = dtype == MOE_F32 ? 4 : 8;
+    return (uintptr_t)out % 16 == 0 && ld % n == 0 && cols % n == 0;
+}
+
+}  // namespace
+
+#define TRY(expr)                         \
+    do {                                  \
+        const int rc_ = (expr);           \
+        if (rc_ != MOE_OK) return rc_;    \
+    } while (0)
+
+extern "C" {
+
+int moe_grouped_product(int32_t n_exp, const int32_t *offsets, int64_t max_rows, const int32_t *gather, int32_t in,
+                        int32_t out, const void *x, int64_t x_ld, const void *w, int32_t y_dtype, void *y, int64_t y_ld,
+                        void *stream) {
+    const char *fn = "moe_grouped_product";
+    TRY(check_product(n_exp, max_rows, in, out, fn));
+    TRY(check_rows(x_ld, in, "x", fn));
+    TRY(check_rows(y_ld, out, "y", fn));
+    TRY(check_out(y_dtype, fn));
+    if (max_rows == 0) return MOE_OK;
+    NEED(offsets);
+    NEED(x);
+    NEED(w);
+    NEED(y);
+    ALIGNED(x, 2);
+    ALIGNED(w, 2);
+    ALIGNED(y, esize(y_dtype));
+    ProductPass p{};
+    p.n_exp = n_exp;
+    p.offsets = offsets;
+    p.max_rows = max_rows;
+    p.gather = gather;
+    p.a = w;
+    p.a_ld = in;
+    p.a_mat = (int64_t)in * out;
+    p.b = x;
+    p.b_ld = x_ld;
+    p.A = out;
+    p.K = in;
+    p.out = y;
+    p.out_ld = y_ld;
+    p.out_f32 = y_dtype == MOE_F32;
+    p.wide = wide_rows(y, y_ld, out, y_dtype);
+    HIPCHK(launch_product(DT_BF16, PRODUCT_Y, p, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+int moe_grouped_product_dx(int32_t n_exp, const int32_t *offsets, int64_t max_rows, int32_t in, int32_t out,
+                           const void *dy, int64_t dy_ld, const void *w, int32_t dx_dtype, void *dx, int64_t dx_ld,
+                           void *stream) {
+    const char *fn = "moe_grouped_product_dx";
+    TRY(check_product(n_exp, max_rows, in, out, fn));
+    TRY(check_rows(dy_ld, out, "dy", fn));
+    TRY(check_rows(dx_ld, in, "dx", fn));
+    TRY(check_out(dx_dtype, fn));
+    if (max_rows == 0) return MOE_OK;
+    NEED(offsets);
+    NEED(dy);
+    NEED(w);
+    NEED(dx);
+    ALIGNED(dy, 2);
+    ALIGNED(w, 2);
+    ALIGNED(dx, esize(dx_dtype));
+    ProductPass p{};
+    p.n_exp = n_exp;
+    p.offsets = offsets;
+    p.max_rows = max_rows;
+    p.a = w;
+    p.a_ld = in;
+    p.a_mat = (int64_t)in * out;
+    p.b = dy;
+    p.b_ld = dy_ld;
+    p.A = in;
+    p.K = out;
+    p.out = dx;
+    p.out_ld = dx_ld;
+    p.out_f32 = dx_dtype == MOE_F32;
+    p.wide = wide_rows(dx, dx_ld, in, dx_dtype);
+    HIPCHK(launch_product(DT_BF16, PRODUCT_DX, p, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+int moe_grouped_product_dw(int32_t n_exp, const int32_t *offsets, int64_t max_rows, const int32_t *gather, int32_t in,
+                           int32_t out, const void *x, int64_t x_ld, const void *dy, int64_t dy_ld, int32_t dw_dtype,
+                           void *dw, int32_t accumulate, void *stream) {
+    const char *fn = "moe_grouped_product_dw";
+    TRY(check_product(n_exp, max_rows, in, out, fn));
+    TRY(check_rows(x_ld, in, "x", fn));
+    TRY(check_rows(dy_ld, out, "dy", fn));
+    TRY(check_out(dw_dtype, fn));
+    if (accumulate && dw_dtype != MOE_F32)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: sums are kept in fp32 alone, not in dtype %d", fn, dw_dtype);
+    NEED(offsets);
+    NEED(dw);
+    if (max_rows > 0) {
+        NEED(x);
+        NEED(dy);
+    }
+    ALIGNED(x, 2);
+    ALIGNED(dy, 2);
+    ALIGNED(dw, esize(dw_dtype));
+    ProductPass p{};
+    p.n_exp = n_exp;
+    p.offsets = offsets;
+    p.max_rows = max_rows;
+    p.gather = gather;
+    p.a = x;
+    p.a_ld = x_ld;
+    p.b = dy;
+    p.b_ld = dy_ld;
+    p.A = in;
+    p.B = out;
+    p.out = dw;
+    p.out_ld = in;
+    p.out_f32 = dw_dtype == MOE_F32;
+    p.accumulate = accumulate != 0;
+    p.wide = wide_rows(dw, in, in, dw_dtype);
+    HIPCHK(launch_product(DT_BF16, PRODUCT_DW, p, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+int moe_quantize_int8(int64_t rows, int32_t cols, int32_t x_dtype, const void *x, int64_t ld, int8_t *q, float *s,
+                      void *stream) {
+    const char *fn = "moe_quantize_int8";
+    TRY(check_mx4_matrix(rows, cols, x_dtype, ld, fn));
+    if (cols > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "%s: cols = %d is too large", fn, cols);
+    if (rows == 0) return MOE_OK;
+    NEED(x);
+    NEED(q);
+    NEED(s);
+    ALIGNED(x, esize(x_dtype));
+    ALIGNED(q, 16);
+    ALIGNED(s, 4);
+    HIPCHK(launch_int8_quantize(dt_of(x_dtype), x, ld, rows, cols, q, s, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+int moe_grouped_product_int8(int32_t n_exp, const int32_t *offsets, int64_t max_rows, const int32_t *gather, int32_t in,
+                             int32_t out, const int8_t *x, const float *x_scales, const int8_t *w, const float *w_scales,
+                             int32_t y_dtype, void *y, int64_t y_ld, void *stream) {
+    const char *fn = "moe_grouped_product_int8";
+    TRY(check_product(n_exp, max_rows, in, out, fn));
+    if (in > 131072) return fail(MOE_ERR_UNSUPPORTED, "%s: in = %d exceeds 131072", fn, in);
+    if (int8_row(in) * out > (1ll << 30))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: in = %d, out = %d are too large for one call", fn, in, out);
+    TRY(check_rows(y_ld, out, "y", fn));
+    TRY(check_out(y_dtype, fn));
+    if (max_rows == 0) return MOE_OK;
+    NEED(offsets);
+    NEED(x);
+    NEED(x_scales);
+    NEED(w);
+    NEED(w_scales);
+    NEED(y);
+    ALIGNED(x, 16);
+    ALIGNED(w, 16);
+    ALIGNED(x_scales, 4);
+    ALIGNED(w_scales, 4);
+    ALIGNED(y, esize(y_dtype));
+    ProductPass p{};
+    p.n_exp = n_exp;
+    p.offsets = offsets;
+    p.max_rows = max_rows;
+    p.gather = gather;
+    p.a = w;
+    p.a_ld = int8_row(in);
+    p.a_mat = p.a_ld * out;
+    p.b = x;
+    p.b_ld = p.a_ld;
+    p.A = out;
+    p.K = (int)p.a_ld;
+    p.out = y;
+    p.out_ld = y_ld;
+    p.out_f32 = y_dtype == MOE_F32;
+    p.wide = wide_rows(y, y_ld, out, y_dtype);
+    p.sa = w_scales;
+    p.sb = x_scales;
+    HIPCHK(launch_product(DT_I8, PRODUCT_Y, p, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+}  // extern "C"

@@ -7,7 +7,7 @@
 
 namespace moe {
 
-enum { DT_F32 = 0, DT_BF16 = 1, DT_E4M3 = 2 };
+enum { DT_F32 = 0, DT_BF16 = 1, DT_E4M3 = 2, DT_I8 = 3 };
 
 // Number of compute units of the current device (cached per device).
 int device_cus();
@@ -61,6 +61,33 @@ struct Mx4Ffn {
     uint16_t *y;            // bf16 [max_rows][d]
 };
 hipError_t launch_mx4_ffn(const Mx4Ffn &a, hipStream_t s);
+
+// ---- products of experts ------------------------------------------------------
+// out[b][a] = sum_k A(a, k) B(b, k) per expert; a is the output's contiguous index.
+//   PRODUCT_Y   A [n_exp][A] rows of K (weights), B rows of K: the row's token of gather; out row per row
+//   PRODUCT_DX  A [n_exp][K] rows of A (weights), B rows of K (dy); out row per row
+//   PRODUCT_DW  A rows of A (x, by gather), B rows of B (dy), the sum over the expert's rows; out [n_exp][B] rows of A
+enum { PRODUCT_Y = 0, PRODUCT_DX = 1, PRODUCT_DW = 2 };
+struct ProductPass {
+    int n_exp;
+    const int32_t *offsets; // [n_exp + 1]
+    int64_t max_rows;
+    const int32_t *gather;  // or null
+    const void *a, *b;
+    int64_t a_ld, b_ld;     // elements between rows
+    int64_t a_mat;          // elements between the experts' matrices
+    int A, B, K;
+    void *out;
+    int64_t out_ld;
+    int out_f32, accumulate;
+    int wide;               // rows of out take 16-byte stores
+    const float *sa, *sb;   // DT_I8: scales of the features [n_exp][A] and of the tokens
+};
+// dt: DT_BF16, or DT_I8 for PRODUCT_Y.
+hipError_t launch_product(int dt, int op, const ProductPass &p, hipStream_t s);
+inline int64_t int8_row(int64_t cols) { return (cols + 127) / 128 * 128; }
+hipError_t launch_int8_quantize(int dt, const void *x, int64_t ld, int64_t rows, int cols, int8_t *q, float *sc,
+                                hipStream_t s);
 
 // ---- dispatch --------------------------------------------------------------
 // Block histogram (64 tokens per block) -> blockcounts[nb][Nr].

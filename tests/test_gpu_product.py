@@ -1,0 +1,248 @@
+"""The grouped products, their gradients and the products in 8-bit integers against the formulas in 64 bits."""
+import math
+
+import pytest
+
+import _product_cases as ref
+from _product_cases import LAYOUTS, SHAPES
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+BF16, FP32 = torch.bfloat16, torch.float32
+IDS = ["%s-%dx%d" % ("_".join(map(str, c)) if len(c) < 9 else "%dx%d" % (len(c), c[0]), i, o) for c, i, o in SHAPES]
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import mixture_experts_layer_35_amd as m
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    m.lib()
+    return m
+
+
+def code(moe, dtype):
+    return moe.MOE_BF16 if dtype == BF16 else moe.MOE_F32
+
+
+def placed(v, dtype, pad, first, fill=math.nan):
+    """v on the GPU as rows of a wider buffer that starts `first` elements behind its allocation; the buffer too."""
+    rows, cols = v.shape
+    flat = torch.full((first + (rows + 1) * (cols + pad),), fill, dtype=dtype, device="cuda")
+    view = flat[first:first + rows * (cols + pad)].view(rows, cols + pad)
+    view[:, :cols] = v.to(dtype)
+    return view[:, :cols], flat
+
+
+def untouched(flat, view, fill):
+    """Whether everything of the buffer outside the view still holds `fill`."""
+    rest = flat.clone()
+    rest.as_strided(view.shape, view.stride(), view.storage_offset()).fill_(fill)
+    return bool((rest == fill).all())
+
+
+def ld(v):
+    return v.stride(0)
+
+
+def dev(t):
+    return None if t is None else t.cuda()
+
+
+@pytest.mark.parametrize("layout", LAYOUTS, ids=lambda v: "_".join(map(str, v)))
+@pytest.mark.parametrize("ydt", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_whole_numbers(moe, shape, ydt, layout):
+    """Sums of whole numbers are exact: every product, gradient and layout gives the formula's value, rounded once."""
+    counts, cin, cout = shape
+    rows, extra = sum(counts), 3
+    xpad, xfirst, ypad, yfirst = layout
+    tokens = max(1, rows // 2)
+    offsets, gather, g = ref.batch(counts, len(counts) + cin, tokens)
+    x, w, dy = ref.integers(g, tokens, cin), ref.integers(g, len(counts), cout, cin), ref.integers(g, rows, cout)
+    xv, _ = placed(x, BF16, xpad, xfirst)
+    dv, _ = placed(torch.cat([dy, torch.full((extra, cout), math.nan)]), BF16, xpad, xfirst)
+    wv = w.to(BF16).cuda()
+    if xfirst:
+        wv = placed(w.reshape(1, -1), BF16, 0, xfirst)[0]
+    o, gd = offsets.cuda(), gather.cuda()
+
+    def call(out_shape, run):
+        v, flat = placed(torch.full(out_shape, 7.0), ydt, ypad, yfirst, 7.0)
+        run(v)
+        torch.cuda.synchronize()
+        return v, flat
+
+    y, flat = call((rows + extra, cout), lambda v: moe.moe_grouped_product(
+        len(counts), o, rows + extra, gd, cin, cout, xv, ld(xv), wv, code(moe, ydt), v, ld(v)))
+    assert (y[:rows].double().cpu() == ref.product(counts, x, gather, w).to(ydt).double()).all()
+    assert (y[rows:] == 7).all() and untouched(flat, y, 7)
+    dx, flat = call((rows + extra, cin), lambda v: moe.moe_grouped_product_dx(
+        len(counts), o, rows + extra, cin, cout, dv, ld(dv), wv, code(moe, ydt), v, ld(v)))
+    assert (dx[:rows].double().cpu() == ref.product_dx(counts, dy, w).to(ydt).double()).all()
+    assert (dx[rows:] == 7).all() and untouched(flat, dx, 7)
+    want = ref.product_dw(counts, x, gather, dy)
+    dw, flat = placed(torch.full((1, want.numel()), 7.0), ydt, 0, yfirst, 7.0)
+    moe.moe_grouped_product_dw(len(counts), o, rows, gd, cin, cout, xv, ld(xv), dv, ld(dv), code(moe, ydt), dw, False)
+    assert (dw.double().cpu().view(want.shape) == want.to(ydt).double()).all() and untouched(flat, dw, 7)
+    if ydt == FP32:
+        moe.moe_grouped_product_dw(len(counts), o, rows, gd, cin, cout, xv, ld(xv), dv, ld(dv), moe.MOE_F32, dw, True)
+        assert (dw.double().cpu().view(want.shape) == 2 * want).all() and untouched(flat, dw, 7)
+
+
+def bound(magnitudes, terms, dtype):
+    """A sum of `terms` products errs by at most a rounding (2^-23, whichever way the unit rounds) an addition, of at
+    most the sum of the magnitudes; then the output's rounding by half a step."""
+    return magnitudes * (terms * 2.0 ** -23) * 1.01, torch.finfo(dtype).eps / 2
+
+
+def near(got, want, magnitudes, terms, dtype):
+    a, r = bound(magnitudes, terms, dtype)
+    got = got.double().cpu()
+    assert got.isfinite().all()
+    off = (got - want).abs() - (a * (1 + r) + r * want.abs())
+    assert (off <= 0).all(), float(off.max())
+
+
+@pytest.mark.parametrize("counts,cin,cout", [([1] * 8, 7168, 2048), ([3, 0, 250, 129, 40], 1000, 360), ([600, 20], 2048, 777)])
+def test_random_values(moe, counts, cin, cout):
+    rows = sum(counts)
+    offsets, gather, g = ref.batch(counts, 5, rows)
+    x, w, dy = (torch.randn(s, generator=g).to(BF16) for s in ((rows, cin), (len(counts), cout, cin), (rows, cout)))
+    o, gd, xd, wd, dd = offsets.cuda(), gather.cuda(), x.cuda(), w.cuda(), dy.cuda()
+    x, w, dy = x.double(), w.double(), dy.double()
+    for dt in (BF16, FP32):
+        y = torch.empty((rows, cout), dtype=dt, device="cuda")
+        moe.moe_grouped_product(len(counts), o, rows, gd, cin, cout, xd, cin, wd, code(moe, dt), y, cout)
+        near(y, ref.product(counts, x, gather, w), ref.product(counts, x.abs(), gather, w.abs()), cin, dt)
+        dx = torch.empty((rows, cin), dtype=dt, device="cuda")
+        moe.moe_grouped_product_dx(len(counts), o, rows, cin, cout, dd, cout, wd, code(moe, dt), dx, cin)
+        near(dx, ref.product_dx(counts, dy, w), ref.product_dx(counts, dy.abs(), w.abs()), cout, dt)
+        dw = torch.empty((len(counts), cout, cin), dtype=dt, device="cuda")
+        moe.moe_grouped_product_dw(len(counts), o, rows, gd, cin, cout, xd, cin, dd, cout, code(moe, dt), dw, False)
+        near(dw, ref.product_dw(counts, x, gather, dy), ref.product_dw(counts, x.abs(), gather, dy.abs()), max(counts), dt)
+
+
+def test_gradients_against_differences(moe):
+    """L = sum of y G: its change along a direction of x and of w is what dx and dw say, exactly for whole numbers."""
+    counts, cin, cout = [9, 0, 40], 72, 48
+    offsets, gather, g = ref.batch(counts, 8, 30)
+    rows = sum(counts)
+    x, w, G = ref.integers(g, 30, cin), ref.integers(g, 3, cout, cin), ref.integers(g, rows, cout)
+    X, W = ref.integers(g, 30, cin), ref.integers(g, 3, cout, cin)
+    o, gd = offsets.cuda(), gather.cuda()
+
+    def loss(x, w):
+        y = torch.empty((rows, cout), device="cuda")
+        moe.moe_grouped_product(3, o, rows, gd, cin, cout, x.to(BF16).cuda(), cin, w.to(BF16).cuda(), moe.MOE_F32, y, cout)
+        return float((y.double().cpu() * G).sum())
+
+    dx = torch.empty((rows, cin), device="cuda")
+    dw = torch.empty((3, cout, cin), device="cuda")
+    Gd = G.to(BF16).cuda()
+    moe.moe_grouped_product_dx(3, o, rows, cin, cout, Gd, cout, w.to(BF16).cuda(), moe.MOE_F32, dx, cin)
+    moe.moe_grouped_product_dw(3, o, rows, gd, cin, cout, x.to(BF16).cuda(), cin, Gd, cout, moe.MOE_F32, dw, False)
+    assert loss(x + X, w) - loss(x - X, w) == 2 * float((dx.double().cpu() * X[gather.long()]).sum())
+    assert loss(x, w + W) - loss(x, w - W) == 2 * float((dw.double().cpu() * W).sum())
+
+
+@pytest.mark.parametrize("cin,cout", [(264, 72), (261, 75)], ids=["pieces", "odd"])
+def test_infinities_and_nan_stay_where_they_belong(moe, cin, cout):
+    counts = [5, 40, 0, 7]
+    rows = sum(counts)
+    offsets, _, g = ref.batch(counts, 3)
+    x, w, dy = ref.integers(g, rows, cin), ref.integers(g, 4, cout, cin), ref.integers(g, rows, cout)
+    x[11, 3], x[20, cin - 1], w[1, 7, cin - 1], w[3, 0, 0] = math.nan, math.inf, math.nan, -math.inf
+    dy[2, cout - 1], dy[47, 0] = math.nan, math.inf
+    o, xd, wd, dd = offsets.cuda(), x.to(BF16).cuda(), w.to(BF16).cuda(), dy.to(BF16).cuda()
+    y = torch.empty((rows, cout), device="cuda")
+    moe.moe_grouped_product(4, o, rows, None, cin, cout, xd, cin, wd, moe.MOE_F32, y, cout)
+    dx = torch.empty((rows, cin), device="cuda")
+    moe.moe_grouped_product_dx(4, o, rows, cin, cout, dd, cout, wd, moe.MOE_F32, dx, cin)
+    dw = torch.empty((4, cout, cin), device="cuda")
+    moe.moe_grouped_product_dw(4, o, rows, None, cin, cout, xd, cin, dd, cout, moe.MOE_F32, dw, False)
+    for got, want in ((y, ref.product(counts, x, None, w)), (dx, ref.product_dx(counts, dy, w)),
+                      (dw, ref.product_dw(counts, x, None, dy))):
+        got = got.double().cpu()
+        fine = want.isfinite()
+        assert (got.isfinite() == fine).all() and (got[fine] == want[fine]).all()
+        inf = want.isinf()
+        assert (got[inf] == want[inf]).all() and fine.any() and not fine.all()
+
+
+# ---- 8-bit integers -----------------------------------------------------------------------------
+
+
+def samples(rows, cols, dtype, g):
+    x = torch.randn((rows, cols), generator=g) * torch.exp2(torch.randint(-60, 60, (rows, 1), generator=g).float())
+    if rows > 5:
+        x[0] = 0.0
+        x[1] = torch.arange(cols) % 128 - 63.5                         # ties, where 63.5 is the largest
+        x[2] = 2.0 ** -120
+        x[3] = torch.finfo(dtype).max
+        x[4] = 2.0 ** -100 * (torch.arange(cols) % 3 - 1)
+        x[5, 1:] = 0.0
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (7, 3), (9, 127), (6, 128), (40, 129), (33, 1000), (5, 2049), (3, 7168),
+                                       (6, 20000)])
+@pytest.mark.parametrize("dtype", [FP32, BF16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("pad,first", [(0, 0), (3, 1), (8, 8)])
+def test_rounding(moe, rows, cols, dtype, pad, first):
+    g = torch.Generator().manual_seed(rows * cols)
+    x = samples(rows, cols, dtype, g)
+    v, _ = placed(x, dtype, pad, first)
+    run = -(-cols // 128) * 128
+    q = torch.full((rows + 1, run), 99, dtype=torch.int8, device="cuda")
+    s = torch.full((rows + 1,), 99.0, device="cuda")
+    moe.moe_quantize_int8(rows, cols, code(moe, dtype), v, ld(v), q, s)
+    wq, ws = ref.quantize(x)
+    assert (q[:rows, :cols].cpu().float() == wq).all() and (q[:rows, cols:] == 0).all() and (q[rows:] == 99).all()
+    assert (s[:rows].cpu() == ws).all() and (s[rows:] == 99).all()
+
+
+def test_rounding_of_rows_that_are_not_finite(moe):
+    x = torch.randn(5, 300)
+    x[1, 299], x[2, 0], x[4, 130] = math.nan, math.inf, -math.inf
+    q = torch.empty((5, 384), dtype=torch.int8, device="cuda")
+    s = torch.empty(5, device="cuda")
+    moe.moe_quantize_int8(5, 300, moe.MOE_F32, x.cuda(), 300, q, s)
+    wq, ws = ref.quantize(x)
+    assert (q[:, :300].cpu().float() == wq).all() and (s.isnan().cpu() == ws.isnan()).all()
+    assert (s.cpu()[[0, 3]] == ws[[0, 3]]).all()
+
+
+@pytest.mark.parametrize("ydt", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("shape", SHAPES + [([2, 0, 1], 7168, 512), ([3], 131072, 9)],
+                         ids=IDS + ["2_0_1-7168x512", "3-131072x9"])
+def test_integer_product(moe, shape, ydt):
+    """Sums of codes are exact, so y is the formula's value but for the two scales' products and the output's rounding."""
+    counts, cin, cout = shape
+    rows, run = sum(counts), -(-cin // 128) * 128
+    tokens = max(1, rows // 2)
+    offsets, gather, g = ref.batch(counts, cin, tokens)
+    x = torch.randint(-127, 128, (tokens, cin), generator=g).to(torch.int8)
+    w = torch.randint(-127, 128, (len(counts), cout, cin), generator=g).to(torch.int8)
+    if cin == 131072:
+        x[:], w[:] = 127, 127                                           # the largest sum there is
+    xs, ws = torch.rand(tokens, generator=g) + 0.5, torch.rand((len(counts), cout), generator=g) + 0.5
+    if tokens > 3:
+        xs[1] = math.nan
+    xq = torch.zeros((tokens, run), dtype=torch.int8)
+    xq[:, :cin] = x
+    wq = torch.zeros((len(counts), cout, run), dtype=torch.int8)
+    wq[..., :cin] = w
+    y, flat = placed(torch.full((rows + 2, cout), 7.0), ydt, 3, 1, 7.0)
+    moe.moe_grouped_product_int8(len(counts), offsets.cuda(), rows + 2, gather.cuda(), cin, cout, xq.cuda(), xs.cuda(),
+                                 wq.cuda(), ws.cuda(), code(moe, ydt), y, ld(y))
+    sums = ref.product(counts, x.double(), gather, w.double())
+    xr = xs.double()[gather.long()][:, None]
+    wr = torch.cat([ws[e].double().expand(hi - lo, cout) for e, lo, hi in ref.spans(counts)])
+    want = sums * xr * wr
+    got = y[:rows].double().cpu()
+    assert (got.isnan() == want.isnan()).all()
+    fine = ~want.isnan()
+    # the sum's conversion and two products, then the output: each at most half a step
+    most = (1 + 2.0 ** -24) ** 3 * (1 + torch.finfo(ydt).eps / 2) - 1
+    assert ((got - want).abs()[fine] <= most * 1.0001 * want.abs()[fine]).all()
+    assert (y[rows:] == 7).all() and untouched(flat, y, 7)
