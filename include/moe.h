@@ -547,6 +547,30 @@ int moe_grouped_product_int8(int32_t n_exp, const int32_t *offsets, int64_t max_
                              int32_t y_dtype, void *y, int64_t y_ld, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* an optimiser's step on the experts' matrices                             */
+
+/*
+ * moe_orthogonalize -- brings each of n matrices g [n][rows][cols] (dense, g_dtype MOE_F32 or MOE_BF16) near its
+ * nearest orthogonal matrix by Newton-Schulz steps, as the Muon optimiser does with the momentum of a weight's gradient:
+ *   X = g / (|g|_F + eps), turned over where rows > cols;
+ *   for each step k:  S = X X^T,  X <- a_k X + (b_k S + c_k S S) X;
+ *   y = scale * X, turned back, bf16 [n][rows][cols] dense.
+ * coeffs (host) holds a_k, b_k, c_k of the steps in turn, 3 * steps floats; 1 <= steps <= 64; eps >= 0.
+ * The norm is held in 64 bits; X, S and their products in pairs of bf16, which keep 16 significant bits, with sums in fp32.
+ * A matrix of zeros gives zeros (with eps > 0), one that holds an infinity or NaN gives NaN; other matrices do not
+ * change.  Deterministic: sums depend on n, rows, cols and the card alone.  y may be g where g is bf16.
+ * With sides rounded up to multiples of 32: a matrix of at most 2^28 values, n of them below 2^40; the smaller side at
+ * most 16384, n at most 65535.
+ * ws: moe_orthogonalize_workspace_bytes(n, rows, cols).
+ */
+int moe_orthogonalize(int64_t n, int32_t rows, int32_t cols, int32_t g_dtype, const void *g, int32_t steps,
+                      const float *coeffs, float eps, float scale, void *y, void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes for moe_orthogonalize: 8 r (r + c) a matrix, r and c its smaller and larger side rounded up to
+ * multiples of 32, and up to 512 more a matrix and 1024 (0 when rejected). */
+size_t moe_orthogonalize_workspace_bytes(int64_t n, int32_t rows, int32_t cols);
+
+/* ------------------------------------------------------------------------ */
 /* helpers                                                                  */
 
 enum { MOE_WS_ROUTE = 0, MOE_WS_PERMUTE = 1, MOE_WS_FORWARD = 2 };

@@ -38,7 +38,7 @@ EXPORTED = ("moe_route", "moe_permute", "moe_grouped_ffn", "moe_combine", "moe_f
             "moe_quantize_1x128", "moe_quantize_weights_128x128", "moe_quantize_128x1", "moe_gate",
             "moe_gate_backward", "moe_quantize_mx4", "moe_dequantize_mx4", "moe_grouped_ffn_mx4",
             "moe_ffn_mx4_workspace_bytes", "moe_grouped_product", "moe_grouped_product_dx", "moe_grouped_product_dw",
-            "moe_quantize_int8", "moe_grouped_product_int8", "moe_last_error", "moe_version")
+            "moe_quantize_int8", "moe_grouped_product_int8", "moe_orthogonalize", "moe_orthogonalize_workspace_bytes", "moe_last_error", "moe_version")
 
 
 class MoeError(RuntimeError):
@@ -128,6 +128,7 @@ def lib():
                 "moe_grouped_product": [i32, P, i64, P, i32, i32, P, i64, P, i32, P, i64, P],
                 "moe_grouped_product_dx": [i32, P, i64, i32, i32, P, i64, P, i32, P, i64, P],
                 "moe_grouped_product_dw": [i32, P, i64, P, i32, i32, P, i64, P, i64, i32, P, i32, P],
+                "moe_orthogonalize": [i64, i32, i32, i32, P, i32, P, ctypes.c_float, ctypes.c_float, P, P, sz, P],
                 "moe_quantize_int8": [i64, i32, i32, P, i64, P, P, P],
                 "moe_grouped_product_int8": [i32, P, i64, P, i32, i32, P, P, P, P, i32, P, i64, P],
             }
@@ -145,6 +146,8 @@ def lib():
             L.moe_backward_workspace_bytes.restype = sz
             L.moe_ffn_mx4_workspace_bytes.argtypes = [i64, i32]
             L.moe_ffn_mx4_workspace_bytes.restype = sz
+            L.moe_orthogonalize_workspace_bytes.argtypes = [i64, i32, i32]
+            L.moe_orthogonalize_workspace_bytes.restype = sz
             L.moe_last_error.argtypes = []
             L.moe_last_error.restype = ctypes.c_char_p
             L.moe_version.argtypes = []
@@ -425,3 +428,19 @@ def moe_grouped_product_int8(n_exp, offsets, max_rows, gather, in_, out, x, x_sc
     return _check(lib().moe_grouped_product_int8(n_exp, _ptr(offsets), max_rows, _ptr(gather), in_, out, _ptr(x),
                                                  _ptr(x_scales), _ptr(w), _ptr(w_scales), y_dtype, _ptr(y), y_ld,
                                                  _stream(stream)))
+
+
+def moe_orthogonalize_workspace_bytes(n: int, rows: int, cols: int) -> int:
+    b = lib().moe_orthogonalize_workspace_bytes(n, rows, cols)
+    if b == 0 and n > 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, moe_last_error())
+    return b
+
+
+def moe_orthogonalize(n, rows, cols, g_dtype, g, steps, coeffs, eps, scale, y, ws, stream=None):
+    """coeffs: 3 * steps numbers, a b c of each step."""
+    if len(coeffs) != 3 * steps:
+        raise ValueError("%d coefficients for %d steps" % (len(coeffs), steps))
+    arr = (ctypes.c_float * max(1, len(coeffs)))(*coeffs)
+    return _check(lib().moe_orthogonalize(n, rows, cols, g_dtype, _ptr(g), steps, ctypes.cast(arr, ctypes.c_void_p), eps,
+                                          scale, _ptr(y), _ptr(ws), _nbytes(ws), _stream(stream)))

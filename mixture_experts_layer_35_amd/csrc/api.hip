@@ -1303,6 +1303,17 @@ int check_out(int32_t dtype, const char *fn) {
     return MOE_OK;
 }
 
+// A matrix is addressed in 32 bits, tiles and launches are counted in 32 bits.
+int check_orthogonalize(int64_t n, int32_t rows, int32_t cols, const char *fn) {
+    if (n < 0 || rows <= 0 || cols <= 0) return fail(MOE_ERR_INVALID_ARG, "%s: sizes must be positive (n >= 0)", fn);
+    const OrthSizes z = orth_sizes(1, rows, cols);
+    const int64_t size = z.rp * z.cp;
+    if (n > 65535 || size > (1ll << 28) || z.r > 16384 || n * size >= (1ll << 40))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: %lld matrices of %d x %d are too large for one call", fn, (long long)n, rows,
+                    cols);
+    return MOE_OK;
+}
+
 // Rows of `out` that take 16-byte stores.
 int wide_rows(const void *out, int64_t ld, int32_t cols, int32_t dtype) {
     const int n = dtype == MOE_F32 ? 4 : 8;
@@ -1486,6 +1497,42 @@ int moe_grouped_product_int8(int32_t n_exp, const int32_t *offsets, int64_t max_
     p.sa = w_scales;
     p.sb = x_scales;
     HIPCHK(launch_product(DT_I8, PRODUCT_Y, p, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+size_t moe_orthogonalize_workspace_bytes(int64_t n, int32_t rows, int32_t cols) {
+    if (check_orthogonalize(n, rows, cols, "moe_orthogonalize_workspace_bytes") != MOE_OK) return 0;
+    const OrthSizes z = orth_sizes(n, rows, cols);
+    return z.norm + 2 * align256(z.x) + 2 * align256(z.s);
+}
+
+int moe_orthogonalize(int64_t n, int32_t rows, int32_t cols, int32_t g_dtype, const void *g, int32_t steps,
+                      const float *coeffs, float eps, float scale, void *y, void *ws, size_t ws_bytes, void *stream) {
+    const char *fn = "moe_orthogonalize";
+    TRY(check_orthogonalize(n, rows, cols, fn));
+    if (g_dtype != MOE_F32 && g_dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: dtype %d", fn, g_dtype);
+    if (steps < 1 || steps > 64) return fail(MOE_ERR_INVALID_ARG, "%s: %d steps", fn, steps);
+    if (!(eps >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "%s: eps = %g", fn, (double)eps);
+    NEED(coeffs);
+    if (n == 0) return MOE_OK;
+    NEED(g);
+    NEED(y);
+    ALIGNED(g, esize(g_dtype));
+    ALIGNED(y, 2);
+    TRY(ws_check(ws, ws_bytes, moe_orthogonalize_workspace_bytes(n, rows, cols), fn));
+    OrthProblem p{};
+    p.n = n;
+    p.rows = rows;
+    p.cols = cols;
+    p.dt = dt_of(g_dtype);
+    p.g = g;
+    p.steps = steps;
+    p.coeffs = coeffs;
+    p.eps = eps;
+    p.scale = scale;
+    p.y = y;
+    p.ws = ws;
+    HIPCHK(launch_orthogonalize(p, (hipStream_t)stream));
     return MOE_OK;
 }
 

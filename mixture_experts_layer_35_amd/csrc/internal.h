@@ -89,6 +89,26 @@ inline int64_t int8_row(int64_t cols) { return (cols + 127) / 128 * 128; }
 hipError_t launch_int8_quantize(int dt, const void *x, int64_t ld, int64_t rows, int cols, int8_t *q, float *sc,
                                 hipStream_t s);
 
+// ---- orthogonalised updates ----------------------------------------------------
+struct OrthProblem {
+    int64_t n, rows, cols;
+    int dt;                 // of g: DT_F32 | DT_BF16
+    const void *g;
+    int steps;
+    const float *coeffs;    // host, a b c of each step
+    double eps;
+    float scale;
+    void *y, *ws;
+};
+struct OrthSizes {
+    int tall;               // more rows than columns: worked on turned over
+    int64_t r, c, rp, cp;   // sides of X, and padded
+    int parts;              // of a matrix's norm
+    size_t x, s, norm;      // bytes of X, of X X^T, of the norms' parts
+};
+OrthSizes orth_sizes(int64_t n, int64_t rows, int64_t cols);
+hipError_t launch_orthogonalize(const OrthProblem &p, hipStream_t s);
+
 // ---- dispatch --------------------------------------------------------------
 // Block histogram (64 tokens per block) -> blockcounts[nb][Nr].
 hipError_t launch_perm_hist(const int32_t *topk_idx, int64_t T, int K, int Nr, int32_t *blockcounts,

@@ -1,0 +1,433 @@
+// orthogonalize.hip -- an update's matrices brought near the nearest orthogonal ones by Newton-Schulz steps:
+//   X_0 = G / (|G|_F + eps);   S = X X^T,  P = b S + c S S,  X <- a X + P X
+// with G transposed where it has more rows than columns.
+//
+// X, S and P are held as pairs of bf16, hi = the nearest bf16 and lo = that of what is left: 2^-16 of a value at most is lost
+// (a step multiplies the smallest singular values, and errors beside them, by up to a = 3.4, so plain bf16 would
+// leave a few percent), and a product of pairs is three matrix products, hi hi + hi lo + lo hi, summed in fp32: lo lo is below
+// what the pair drops.  Rows of pairs hold 32 hi and then 32 lo of 32 values in turn, 128 bytes, which is what a step of the
+// reduction takes from a row.  Sides are padded to multiples of 32 with zeros.
+#include <atomic>
+#include <type_traits>
+
+#include "common.h"
+#include "internal.h"
+#include "lds_ring.h"
+#include "strided.h"
+#include "variants.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kOrthThreads = 512;
+
+// hi and lo of a value; a value that is not finite gives NaN in lo and so in every sum it meets.
+__device__ __forceinline__ void split_pair(float v, float &hi, float &lo) {
+    hi = bf16_to_f32((uint16_t)pack_bf16x2(v, 0.0f));
+    lo = v - hi;
+}
+
+// ---- norms and the first X ---------------------------------------------------
+
+constexpr int kNormThreads = 256;
+
+template <int DT>
+__device__ __forceinline__ float load_value(const void *g, int64_t i) {
+    return DT == DT_F32 ? ((const float *)g)[i] : bf16_to_f32(((const uint16_t *)g)[i]);
+}
+
+// part[m][p]: the sum of the squares of a share of matrix m, in 64 bits (no square of an fp32 value leaves them).
+template <int DT>
+__global__ __launch_bounds__(kNormThreads) void orth_norm_kernel(const void *__restrict__ g, int64_t size, int parts,
+                                                                 double *__restrict__ part) {
+    const int m = blockIdx.x / parts, p = blockIdx.x % parts;
+    const int64_t from = size * p / parts, to = size * (p + 1) / parts;
+    double sum = 0.0;
+    for (int64_t i = from + threadIdx.x; i < to; i += kNormThreads) {
+        const double v = load_value<DT>(g, m * size + i);
+        sum += v * v;
+    }
+    __shared__ double all[kNormThreads];
+    all[threadIdx.x] = sum;
+    __syncthreads();
+    for (int w = kNormThreads / 2; w > 0; w >>= 1) {
+        if ((int)threadIdx.x < w) all[threadIdx.x] += all[threadIdx.x + w];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) part[blockIdx.x] = all[0];
+}
+
+// X_0 in pairs: a workgroup takes 32 x 32 values, of G^T where `tall`.
+template <int DT>
+__global__ __launch_bounds__(256) void orth_first_kernel(const void *__restrict__ g, const double *__restrict__ part,
+                                                         int parts, double eps, int tall, int r, int c, int rp, int cp,
+                                                         uint16_t *__restrict__ x) {
+    const int m = blockIdx.z, c0 = blockIdx.x * 32, r0 = blockIdx.y * 32;
+    double sum = 0.0;
+    for (int p = 0; p < parts; ++p) sum += part[m * parts + p];
+    const double inv = 1.0 / (sqrt(sum) + eps);
+    __shared__ float v[32][33];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+#pragma unroll
+    for (int k = 0; k < 32; k += 8) {
+        // (row, column) of X; lanes run along G's rows
+        const int i = tall ? r0 + tx : r0 + ty + k, j = tall ? c0 + ty + k : c0 + tx;
+        const int64_t at = (int64_t)m * r * c + (tall ? (int64_t)j * r + i : (int64_t)i * c + j);
+        v[i - r0][j - c0] = i < r && j < c ? (float)((double)load_value<DT>(g, at) * inv) : 0.0f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 32; k += 8) {
+        const int i = r0 + ty + k;
+        float hi, lo;
+        split_pair(v[ty + k][tx], hi, lo);
+        uint16_t *row = x + ((int64_t)m * rp + i) * cp * 2 + c0 * 2;
+        row[tx] = (uint16_t)pack_bf16x2(hi, 0.0f);
+        row[32 + tx] = (uint16_t)pack_bf16x2(lo, 0.0f);
+    }
+}
+
+// ---- products ----------------------------------------------------------------
+
+// out[b][a] = sum over k of A(a, k) B(b, k):
+//   GRAM    A, B: rows of X, k along them         S, symmetric
+//   SQUARE  A, B: rows of S                       P = c S S + b S, symmetric
+//   UPDATE  A: columns of X (k: its rows), B: rows of P      a X + P X
+enum { ORTH_GRAM, ORTH_SQUARE, ORTH_UPDATE };
+
+struct OrthPass {
+    int n;
+    int A, B, K;                // sides of out, padded, and the reduction's length
+    const uint16_t *a, *b;      // pairs; rows of K (A: UPDATE rows of A)
+    const uint16_t *c;          // what the epilogue adds, as out
+    float alpha, beta;          // out = alpha * sum + beta * c
+    uint16_t *out;              // pairs, or
+    uint16_t *y;                // the result, bf16, [rows][cols] of G
+    int r, cc, tall;            // sides of X without padding
+};
+
+// A tile is 64 RB values of a against 32 CAP of b; eight waves, 4 along a by 2 along b (16-row blocks of b in turn).
+template <int RB, int CAP>
+struct OrthTile {
+    static constexpr int TA = RB * 64, TB = CAP * 32;
+    static constexpr int stage_a = TA * 128, stage = stage_a + TB * 128;
+    static constexpr int scratch = 8 * 16 * 17 * 4;     // a 16 x 16 block of each wave, turned over
+    static constexpr int slots = (160 * 1024 - scratch) / stage < 4 ? (160 * 1024 - scratch) / stage : 4;
+    static constexpr int lds = slots * stage + scratch;
+};
+
+template <int OP, int RB, int CAP>
+__global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a) {
+    typedef OrthTile<RB, CAP> T;
+    constexpr bool SYM = OP != ORTH_UPDATE, ASTRIDED = OP == ORTH_UPDATE;
+    constexpr int SLOTS = T::slots, STAGE = T::stage, QB = CAP / 2, N = RB + QB;
+    static_assert(CAP % 2 == 0 && SLOTS >= 2, "loads of a step are shared evenly");
+    extern __shared__ __align__(1024) char smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    char *const ring = smem;
+    uint32_t *const turn = (uint32_t *)(smem + SLOTS * STAGE) + wid * (16 * 17);
+    const int at = (a.A + T::TA - 1) / T::TA, bt = (a.B + T::TB - 1) / T::TB;
+    // symmetric: the tiles that reach the diagonal or lie below it (b >= a), for each column of tiles a run of them
+    auto tiles_below = [&](int ia) { return bt - min(bt, ia * T::TA / T::TB); };
+    int per_matrix = at * bt;
+    if (SYM) {
+        per_matrix = 0;
+        for (int i = 0; i < at; ++i) per_matrix += tiles_below(i);
+    }
+    const int total = a.n * per_matrix;
+    const int per = (total + 7) / 8, xcd = blockIdx.x & 7;
+    const int end = min(total, (xcd + 1) * per), first = xcd * per + (blockIdx.x >> 3), step = gridDim.x >> 3;
+    if (first >= end) return;
+    auto find = [&](int t, int &m, int &a0, int &b0) {
+        m = __builtin_amdgcn_readfirstlane(t / per_matrix);
+        int rest = t - m * per_matrix, ia = 0;
+        if (SYM) {
+            for (int k = tiles_below(0); rest >= k; k = tiles_below(ia)) {
+                rest -= k;
+                ++ia;
+            }
+            b0 = (bt - tiles_below(ia) + rest) * T::TB;
+        } else {
+            ia = __builtin_amdgcn_readfirstlane(rest / bt);
+            b0 = (rest - ia * bt) * T::TB;
+        }
+        a0 = ia * T::TA;
+    };
+    const int steps = a.K / 32;
+
+    // ---- loads ----
+    int it = first, ik = 0;
+    __amdgpu_buffer_rsrc_t ar, br;
+    uint32_t avoff[RB], bvoff[QB];
+    const int a_step = ASTRIDED ? 32 * a.A * 4 : 128;
+    auto bytes_at = [&](int row) { return ((lane & 7) ^ swz<128>(row)) << 4; };
+    auto aim = [&]() {
+        int m, a0, b0;
+        find(it, m, a0, b0);
+        const int64_t amat = (int64_t)(ASTRIDED ? a.K : a.A) * (ASTRIDED ? a.A : a.K) * 2, bmat = (int64_t)a.B * a.K * 2;
+        ar = buffer_of(a.a + m * amat, amat * 2);
+        br = buffer_of(a.b + m * bmat, bmat * 2);
+#pragma unroll
+        for (int q = 0; q < RB; ++q) {
+            if (ASTRIDED) {
+                // 16 bytes number (lane, or its low half) of row k of the step
+                const int k = RB == 4 ? wid * 4 + q : wid * 4 + q * 2 + (lane >> 5);
+                const int piece = (RB == 4 ? lane : lane & 31) ^ strided_slot(k);
+                const int col = a0 * 4 + piece * 16;
+                avoff[q] = col < a.A * 4 ? (uint32_t)(k * a.A * 4 + col) : kNoOffset;
+            } else {
+                const int row = wid * (RB * 8) + q * 8 + (lane >> 3);
+                avoff[q] = a0 + row < a.A ? (uint32_t)((a0 + row) * a.K * 4 + bytes_at(row)) : kNoOffset;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < QB; ++q) {
+            const int row = (q * 8 + wid) * 8 + (lane >> 3);
+            bvoff[q] = b0 + row < a.B ? (uint32_t)((b0 + row) * a.K * 4 + bytes_at(row)) : kNoOffset;
+        }
+    };
+    // issues a step's N loads; 0 behind the last tile
+    auto issue = [&](int slot) {
+        if (it >= end) return 0;
+        if (ik == 0) aim();
+        char *as = ring + slot * STAGE + wid * (RB * 1024), *bs = ring + slot * STAGE + T::stage_a + wid * 1024;
+#pragma unroll
+        for (int q = 0; q < RB; ++q) buffer_dma16(ar, avoff[q], ik * a_step, as + q * 1024);
+#pragma unroll
+        for (int q = 0; q < QB; ++q) buffer_dma16(br, bvoff[q], ik * 128, bs + q * 8192);
+        if (++ik == steps) {
+            ik = 0;
+            it += step;
+        }
+        return N;
+    };
+
+    // ---- products ----
+    const int wf = wid >> 1, wm = wid & 1, r15 = lane & 15, g = lane >> 4;
+    const int arow = wf * (RB * 16) + r15, brow = wm * 16 + r15;
+    const int alo = arow * 128 + ((g ^ swz<128>(arow)) << 4), blo = brow * 128 + ((g ^ swz<128>(brow)) << 4);
+    int aofs[RB][2];
+    if (ASTRIDED) {
+        const int jj = (lane >> 2) & 3, aa = lane & 3, k = 8 * g + jj;
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int col = wf * (RB * 16) + i * 16 + 4 * aa;
+                const int piece = ((col >> 5) * 128 + p * 64 + (col & 31) * 2) >> 4;
+                aofs[i][p] = k * (RB * 256) + ((piece ^ strided_slot(k)) << 4) + 8 * (aa & 1);
+            }
+    }
+    int slot = 0;
+    auto next = [](int s, int d) { return s + d >= SLOTS ? s + d - SLOTS : s + d; };
+    int later[SLOTS - 1] = {};       // loads of the steps under way, the next one's first
+    issue(0);
+#pragma unroll
+    for (int s = 1; s < SLOTS - 1; ++s) later[s - 1] = issue(s);
+    for (int t = first; t < end; t += step) {
+        f32x4 acc[RB][CAP] = {};
+        for (int k = 0; k < steps; ++k) {
+            int n = 0;
+#pragma unroll
+            for (int s = 0; s < SLOTS - 2; ++s) n += later[s];
+            wait_vmcnt_dyn(n);
+            wait_lgkm0();
+            cta_barrier();
+#pragma unroll
+            for (int s = 0; s + 1 < SLOTS - 2; ++s) later[s] = later[s + 1];
+            n = issue(next(slot, SLOTS - 1));
+            if (SLOTS > 2) later[SLOTS > 2 ? SLOTS - 3 : 0] = n;
+            const char *as = ring + slot * STAGE, *bs = as + T::stage_a;
+            bf16x8 ah[RB], al[RB];
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                if constexpr (ASTRIDED) {
+                    ah[i] = read_strided<RB * 256>(as + aofs[i][0]);
+                    al[i] = read_strided<RB * 256>(as + aofs[i][1]);
+                } else {
+                    ah[i] = *(const bf16x8 *)(as + alo + i * 2048);
+                    al[i] = *(const bf16x8 *)(as + (alo ^ 64) + i * 2048);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < CAP; ++j) {
+                const bf16x8 bh = *(const bf16x8 *)(bs + blo + j * 4096), bl = *(const bf16x8 *)(bs + (blo ^ 64) + j * 4096);
+#pragma unroll
+                for (int i = 0; i < RB; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ah[i], bh, acc[i][j], 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < RB; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ah[i], bl, acc[i][j], 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < RB; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(al[i], bh, acc[i][j], 0, 0, 0);
+            }
+            slot = next(slot, 1);
+        }
+        // ---- results ----
+        int m, a0, b0;
+        find(t, m, a0, b0);
+        const bool mirror = SYM && b0 >= a0 + T::TA;
+        const int64_t ld = (int64_t)a.A * 2, mat = (int64_t)m * a.B * ld;
+#pragma unroll
+        for (int j = 0; j < CAP; ++j) {
+            const int bb = b0 + (j * 2 + wm) * 16, b = bb + r15;
+#pragma unroll
+            for (int i = 0; i < RB; i += 2) {
+                const int f0 = a0 + wf * (RB * 16) + i * 16;           // a run of 32 values of a
+                const bool there = b < a.B && f0 < a.A;
+                float v[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    u32x2 ch = {0, 0}, cl = {0, 0};
+                    if (OP != ORTH_GRAM && there) {
+                        const uint16_t *row = a.c + mat + b * ld + f0 * 2 + h * 16 + 4 * g;
+                        ch = *(const u32x2 *)row;
+                        cl = *(const u32x2 *)(row + 32);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float hi = bf16_to_f32((uint16_t)(ch[q >> 1] >> (16 * (q & 1))));
+                        const float lo = bf16_to_f32((uint16_t)(cl[q >> 1] >> (16 * (q & 1))));
+                        v[h][q] = a.alpha * acc[i + h][j][q];
+                        if (OP != ORTH_GRAM) v[h][q] += a.beta * (hi + lo);
+                    }
+                }
+                if (OP == ORTH_UPDATE && a.y) {
+                    const int64_t ym = (int64_t)m * a.r * a.cc;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int f = f0 + h * 16 + 4 * g + q;
+                            if (b < a.r && f < a.cc)
+                                a.y[ym + (a.tall ? (int64_t)f * a.r + b : (int64_t)b * a.cc + f)] =
+                                    (uint16_t)pack_bf16x2(v[h][q], 0.0f);
+                        }
+                    continue;
+                }
+                float hi[2][4], lo[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) split_pair(v[h][q], hi[h][q], lo[h][q]);
+                const u32x4 oh = pair_bf16_value(hi[0], hi[1], lane), ol = pair_bf16_value(lo[0], lo[1], lane);
+                if (there) {
+                    uint16_t *row = a.out + mat + b * ld + f0 * 2 + pair_bf16_col(0, lane);
+                    *(u32x4 *)row = oh;
+                    *(u32x4 *)(row + 32) = ol;
+                }
+                if (mirror) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        // the block [b][a] turned over in the wave's own LDS: lane 4 a + k then holds b = 4 k .. 4 k + 3
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) turn[(4 * g + q) * 17 + r15] = pack_bf16x2(hi[h][q], lo[h][q]);
+                        asm volatile("" ::: "memory");      // LDS serves a wave's writes and reads in order
+                        uint32_t w[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) w[q] = turn[(lane >> 2) * 17 + (lane & 3) * 4 + q];
+                        asm volatile("" ::: "memory");
+                        const int f = f0 + h * 16 + (lane >> 2);
+                        if (f < a.A && bb < a.B) {
+                            uint16_t *row = a.out + mat + f * ld + (bb >> 5) * 64 + (bb & 31) + (lane & 3) * 4;
+                            *(u32x2 *)row = u32x2{w[0] & 0xFFFF | w[1] << 16, w[2] & 0xFFFF | w[3] << 16};
+                            *(u32x2 *)(row + 32) = u32x2{w[0] >> 16 | w[1] & 0xFFFF0000u, w[2] >> 16 | w[3] & 0xFFFF0000u};
+                        }
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <void (*KERNEL)(OrthPass)>
+hipError_t orth_launch(unsigned grid, int lds, const OrthPass &p, hipStream_t s) {
+    static std::atomic<uint64_t> allowed{0};
+    const hipError_t e = allow_lds((const void *)KERNEL, lds, allowed);
+    if (e != hipSuccess) return e;
+    KERNEL<<<grid, kOrthThreads, lds, s>>>(p);
+    return hipGetLastError();
+}
+
+template <int OP>
+hipError_t orth_product(const OrthPass &p, hipStream_t s) {
+    const unsigned grid = (unsigned)((device_cus() + 7) / 8 * 8);
+    switch (orth_variant(p.n, p.A, p.B, OP != ORTH_UPDATE, grid)) {
+        case kOrth256x256: return orth_launch<orth_kernel<OP, 4, 8>>(grid, OrthTile<4, 8>::lds, p, s);
+        case kOrth256x128: return orth_launch<orth_kernel<OP, 4, 4>>(grid, OrthTile<4, 4>::lds, p, s);
+        default: return orth_launch<orth_kernel<OP, 2, 4>>(grid, OrthTile<2, 4>::lds, p, s);
+    }
+}
+
+}  // namespace
+
+OrthSizes orth_sizes(int64_t n, int64_t rows, int64_t cols) {
+    OrthSizes z{};
+    z.tall = rows > cols;
+    z.r = z.tall ? cols : rows;
+    z.c = z.tall ? rows : cols;
+    z.rp = (z.r + 31) / 32 * 32;
+    z.cp = (z.c + 31) / 32 * 32;
+    z.parts = (int)(z.r * z.c / 65536 + 1 < 64 ? z.r * z.c / 65536 + 1 : 64);
+    z.x = (size_t)n * z.rp * z.cp * 4;
+    z.s = (size_t)n * z.rp * z.rp * 4;
+    z.norm = ((size_t)n * z.parts * 8 + 255) / 256 * 256;
+    return z;
+}
+
+hipError_t launch_orthogonalize(const OrthProblem &q, hipStream_t s) {
+    const OrthSizes z = orth_sizes(q.n, q.rows, q.cols);
+    char *ws = (char *)q.ws;
+    double *part = (double *)ws;
+    ws += z.norm;
+    uint16_t *x[2], *gram, *poly;
+    auto take = [&](size_t bytes) { uint16_t *p = (uint16_t *)ws; ws += (bytes + 255) / 256 * 256; return p; };
+    x[0] = take(z.x);
+    x[1] = take(z.x);
+    gram = take(z.s);
+    poly = take(z.s);
+    const int n = (int)q.n, r = (int)z.r, c = (int)z.c, rp = (int)z.rp, cp = (int)z.cp;
+    const dim3 blocks(cp / 32, rp / 32, n);
+    if (q.dt == DT_F32) {
+        orth_norm_kernel<DT_F32><<<n * z.parts, kNormThreads, 0, s>>>(q.g, z.r * z.c, z.parts, part);
+        orth_first_kernel<DT_F32><<<blocks, 256, 0, s>>>(q.g, part, z.parts, q.eps, z.tall, r, c, rp, cp, x[0]);
+    } else {
+        orth_norm_kernel<DT_BF16><<<n * z.parts, kNormThreads, 0, s>>>(q.g, z.r * z.c, z.parts, part);
+        orth_first_kernel<DT_BF16><<<blocks, 256, 0, s>>>(q.g, part, z.parts, q.eps, z.tall, r, c, rp, cp, x[0]);
+    }
+    hipError_t e = hipGetLastError();
+    for (int k = 0; k < q.steps && e == hipSuccess; ++k) {
+        const float *co = q.coeffs + 3 * k;
+        OrthPass p{};
+        p.n = n;
+        p.A = p.B = rp;
+        p.K = cp;
+        p.a = p.b = x[k & 1];
+        p.alpha = 1.0f;
+        p.out = gram;
+        e = orth_product<ORTH_GRAM>(p, s);
+        if (e != hipSuccess) break;
+        p.K = rp;
+        p.a = p.b = p.c = gram;
+        p.alpha = co[2];
+        p.beta = co[1];
+        p.out = poly;
+        e = orth_product<ORTH_SQUARE>(p, s);
+        if (e != hipSuccess) break;
+        p.A = cp;
+        p.a = p.c = x[k & 1];
+        p.b = poly;
+        const bool last = k == q.steps - 1;
+        const float scale = last ? q.scale : 1.0f;
+        p.alpha = scale;
+        p.beta = co[0] * scale;
+        p.out = x[(k + 1) & 1];
+        p.y = last ? (uint16_t *)q.y : nullptr;
+        p.r = r;
+        p.cc = c;
+        p.tall = z.tall;
+        e = orth_product<ORTH_UPDATE>(p, s);
+    }
+    return e;
+}
+
+}  // namespace moe

@@ -6,6 +6,7 @@
 #include "common.h"
 #include "internal.h"
 #include "lds_ring.h"
+#include "strided.h"
 #include "tile_list.h"
 #include "variants.h"
 
@@ -54,29 +55,6 @@ struct Product<DT_I8> {
 
 // 16 bytes that lanes without data read.
 __device__ const u32x4 product_zeros = {0, 0, 0, 0};
-
-constexpr uint32_t kNoOffset = 0x80000000u;   // past every descriptor's bytes: reads zeros
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, int64_t bytes) {
-    const uint64_t u = (uint64_t)p;
-    const uint64_t base = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(u >> 32)) << 32 |
-                          (uint32_t)__builtin_amdgcn_readfirstlane((int)u);
-    return __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, __builtin_amdgcn_readfirstlane((int)bytes),
-                                             0x00020000);
-}
-
-// Operands whose rows are the reduction's are staged as they lie in memory, [64 rows][256 values], and read by the LDS
-// transpose read: the 16 lanes of a group address 4 rows x 32 bytes and receive four rows of one value each.  Slots of 16 bytes
-// are permuted so that the eight rows that a read's half wave touches lie in different banks.
-__device__ __forceinline__ int strided_slot(int k) { return 2 * ((k & 3) | (((k >> 3) & 1) << 2)); }
-
-typedef short v4s __attribute__((ext_vector_type(4)));
-typedef short v8s __attribute__((ext_vector_type(8)));
-__device__ __forceinline__ bf16x8 read_strided(const char *p) {
-    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)p);
-    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(p + 4 * 512));
-    return __builtin_bit_cast(bf16x8, (v8s)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-}
 
 // Values e0 .. e0 + 7 of a bf16 row of `n` values at any address, zeros past its end.
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
@@ -338,12 +316,12 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
                 typename P::frag af[4], bf[TB];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if constexpr (ASTRIDED) af[i] = read_strided(as + aofs[i] + s * (32 * 512));
+                    if constexpr (ASTRIDED) af[i] = read_strided<512>(as + aofs[i] + s * (32 * 512));
                     else af[i] = *(const typename P::frag *)(as + (alo ^ (s * 64)) + i * 2048);
                 }
 #pragma unroll
                 for (int j = 0; j < TB; ++j) {
-                    if constexpr (DW) bf[j] = read_strided(bs + bofs[j & 3] + (j >> 2) * 256 + s * (32 * 512));
+                    if constexpr (DW) bf[j] = read_strided<512>(bs + bofs[j & 3] + (j >> 2) * 256 + s * (32 * 512));
                     else bf[j] = *(const typename P::frag *)(bs + (blo ^ (s * 64)) + j * 4096);
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -444,19 +422,11 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
     }
 }
 
-// The kernel's shared memory is allowed once on each device.
 template <void (*KERNEL)(ProductPass)>
 hipError_t product_launch(unsigned grid, int lds, const ProductPass &p, hipStream_t s) {
     static std::atomic<uint64_t> allowed{0};
-    int device = 0;
-    hipError_t e = hipGetDevice(&device);
+    const hipError_t e = allow_lds((const void *)KERNEL, lds, allowed);
     if (e != hipSuccess) return e;
-    const uint64_t bit = 1ull << (device & 63);
-    if (device > 63 || !(allowed.load(std::memory_order_relaxed) & bit)) {
-        e = hipFuncSetAttribute((const void *)KERNEL, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess) return e;
-        allowed.fetch_or(bit, std::memory_order_relaxed);
-    }
     KERNEL<<<grid, kProductThreads, lds, s>>>(p);
     return hipGetLastError();
 }

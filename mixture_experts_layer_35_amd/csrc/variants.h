@@ -61,4 +61,23 @@ inline Mx4Variant mx4_variant(int64_t max_rows, int64_t n_exp, int64_t kruns, in
     return fewer && blocks(kMx4Tile160) * ((ftiles + 3) / 4) >= cus ? kMx4Tile160 : kMx4Tile128;
 }
 
+// ---- orthogonalised updates ----------------------------------------------------
+enum OrthVariant { kOrth256x256, kOrth256x128, kOrth128x128 };   // a tile's sides along a and b
+
+// The tiles that end soonest: rounds of tiles over the workgroups, each as long as its products.
+inline OrthVariant orth_variant(int64_t n, int64_t A, int64_t B, bool symmetric, int64_t workgroups) {
+    auto time = [&](int64_t ta, int64_t tb) {
+        const int64_t at = (A + ta - 1) / ta, bt = (B + tb - 1) / tb;
+        int64_t tiles = 0;
+        for (int64_t i = 0; i < at; ++i) {
+            const int64_t above = symmetric ? i * ta / tb : 0;
+            tiles += bt - (above < bt ? above : bt);
+        }
+        return (n * tiles + workgroups - 1) / workgroups * ta * tb;
+    };
+    const int64_t big = time(256, 256), mid = time(256, 128), small = time(128, 128);
+    if (big <= mid && big <= small) return kOrth256x256;
+    return mid <= small ? kOrth256x128 : kOrth128x128;
+}
+
 }  // namespace moe

@@ -1,0 +1,145 @@
+"""moe_orthogonalize against its formula in 64 bits."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+BF16, FP32 = torch.bfloat16, torch.float32
+MUON = (3.4445, -4.7750, 2.0315)
+CUBIC = (1.5, -0.5, 0.0)
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import mixture_experts_layer_35_amd as m
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    m.lib()
+    return m
+
+
+def run(moe, g, coeffs=MUON * 5, eps=1e-7, scale=1.0, y=None):
+    n, rows, cols = g.shape
+    need = moe.moe_orthogonalize_workspace_bytes(n, rows, cols)
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")      # NaN, wherever it is read unwritten
+    y = torch.full(g.shape, math.nan, dtype=BF16, device="cuda") if y is None else y
+    dt = moe.MOE_BF16 if g.dtype == BF16 else moe.MOE_F32
+    moe.moe_orthogonalize(n, rows, cols, dt, g, len(coeffs) // 3, coeffs, eps, scale, y, ws[:need])
+    torch.cuda.synchronize()
+    assert (ws[need:] == 0xFF).all()
+    return y
+
+
+def exact(g, coeffs=MUON * 5, eps=1e-7, scale=1.0):
+    """The formula for one matrix in 64 bits, and how far (2-norm over all values) pairs of bf16 and sums in fp32 may lead
+    from it.
+
+    In a step every value of X, S, S S and P takes a rounding to a pair and a product's dropped lo lo, of at most 2^-16 of it
+    each, and a sum of K terms one of sqrt(K) 2^-24 (its additions' roundings do not line up): with s the largest singular
+    value of X that is at most u (|a| + 3 |b| s^2 + 5 |c| s^4) |X|, u = 2 * 2^-16 + sqrt(K) 2^-24.  A step p(x) = a x + b x^3 + c x^5 of
+    the singular values carries what came before on by at most the largest |p'| and p(x) / x up to s (an odd function of a
+    matrix's singular values changes by at most its own Lipschitz constant)."""
+    x = g.double()
+    tall = x.shape[0] > x.shape[1]
+    x = x.t() if tall else x
+    x = x / (x.square().sum().sqrt() + eps)
+    off = 2.0 ** -16 * float(x.norm())
+    u = 2 * 2.0 ** -16 + math.sqrt(max(x.shape)) * 2.0 ** -24
+    for k in range(0, len(coeffs), 3):
+        a, b, c = coeffs[k:k + 3]
+        top = float(torch.linalg.matrix_norm(x, 2)) * 1.001 + off
+        t = torch.linspace(0, top, 1000, dtype=torch.float64)
+        grow = float(torch.maximum((a + 3 * b * t ** 2 + 5 * c * t ** 4).abs(), (a + b * t ** 2 + c * t ** 4).abs()).max())
+        off = off * grow + u * (abs(a) + 3 * abs(b) * top ** 2 + 5 * abs(c) * top ** 4) * float(x.norm())
+        s = x @ x.t()
+        x = a * x + (b * s + c * s @ s) @ x
+    return scale * (x.t() if tall else x), abs(scale) * off
+
+
+def check(got, want, off):
+    got = got.double().cpu()
+    assert got.isfinite().all()
+    most = off + 2.0 ** -8 * (float(want.norm()) + off)
+    assert float((got - want).norm()) <= most, (float((got - want).norm()), most)
+
+
+SIZES = [(1, 1, 1), (3, 1, 40), (2, 40, 1), (2, 7, 5), (1, 32, 32), (5, 33, 95), (2, 64, 200), (3, 200, 64), (1, 128, 129),
+         (2, 300, 301), (1, 520, 640), (24, 100, 36), (1, 260, 1500), (40, 96, 96), (1, 1100, 700)]
+
+
+@pytest.mark.parametrize("n,rows,cols", SIZES)
+@pytest.mark.parametrize("dtype", [FP32, BF16], ids=["fp32", "bf16"])
+def test_random_matrices(moe, n, rows, cols, dtype):
+    gen = torch.Generator().manual_seed(rows * cols + n)
+    g = torch.randn((n, rows, cols), generator=gen)
+    if n > 1:
+        g[1] *= 1e-3
+    g = g.to(dtype)
+    y = run(moe, g.cuda())
+    for i in range(n):
+        check(y[i], *exact(g[i]))
+
+
+def test_sizes_take_every_kernel(moe):
+    """Many and few, large and small matrices: each pair of tile sides in each product."""
+    gen = torch.Generator().manual_seed(4)
+    for n, rows, cols in ((8, 700, 1300), (2, 900, 1000), (64, 512, 256), (3, 1536, 160), (16, 768, 800)):
+        g = torch.randn((n, rows, cols), generator=gen)
+        y = run(moe, g.cuda())
+        for i in (0, n - 1):
+            check(y[i], *exact(g[i]))
+
+
+@pytest.mark.parametrize("coeffs", [MUON, CUBIC * 3, MUON * 2 + CUBIC * 2, (0.0, 0.0, 1.0), (0.0, 1.0, 0.0), (2.0, 0.0, 0.0)])
+def test_coefficients_and_scale(moe, coeffs):
+    gen = torch.Generator().manual_seed(9)
+    g = torch.randn((2, 50, 130), generator=gen)
+    for scale in (1.0, -0.25):
+        y = run(moe, g.cuda(), coeffs, 1e-7, scale)
+        for i in range(2):
+            check(y[i], *exact(g[i], coeffs, 1e-7, scale))
+
+
+def test_diagonal_matrices_follow_the_polynomial(moe):
+    """Each singular value by itself; what is 0 stays 0."""
+    d = torch.logspace(-3, 0, 70, dtype=torch.float64).float()
+    g = torch.zeros(1, 70, 100)
+    g[0, torch.arange(70), torch.randperm(100, generator=torch.Generator().manual_seed(1))[:70]] = d
+    y = run(moe, g.cuda())
+    want, off = exact(g[0])
+    check(y[0], want, off)
+    assert ((y[0].cpu() == 0) == (g[0] == 0)).all()
+
+
+def test_a_small_part_of_the_directions(moe):
+    """Rank 3: noise in the other directions would be multiplied by up to 485."""
+    gen = torch.Generator().manual_seed(3)
+    g = (torch.randn((1, 150, 3), generator=gen) @ torch.randn((1, 3, 400), generator=gen))
+    check(run(moe, g.cuda())[0], *exact(g[0]))
+
+
+def test_zeros_and_matrices_that_are_not_finite(moe):
+    g = torch.randn((5, 40, 70), generator=torch.Generator().manual_seed(2))
+    g[1] = 0.0
+    g[2, 3, 4], g[3, 39, 69] = math.nan, math.inf
+    y = run(moe, g.cuda())
+    assert (y[1] == 0).all() and y[2].isnan().all() and y[3].isnan().all()
+    for i in (0, 4):
+        check(y[i], *exact(g[i]))
+    alone = run(moe, g[4:].cuda())
+    assert (alone[0] == y[4]).all()
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e30])
+def test_sizes_whose_squares_leave_32_bits(moe, size):
+    g = torch.randn((1, 40, 70), generator=torch.Generator().manual_seed(2)) * size
+    check(run(moe, g.cuda(), eps=0.0)[0], *exact(g[0], eps=0.0))
+
+
+def test_in_place_and_again(moe):
+    g = torch.randn((3, 96, 200), generator=torch.Generator().manual_seed(2)).to(BF16).cuda()
+    y = run(moe, g)
+    again = run(moe, g)
+    inside = g.clone()
+    run(moe, inside, y=inside)
+    assert (y == again).all() and (y == inside).all()
