@@ -32,21 +32,18 @@ __device__ __forceinline__ void split_pair(float v, float &hi, float &lo) {
 
 constexpr int kNormThreads = 256;
 
-template <int DT>
-__device__ __forceinline__ float load_value(const void *g, int64_t i) {
-    return DT == DT_F32 ? ((const float *)g)[i] : bf16_to_f32(((const uint16_t *)g)[i]);
-}
-
 // part[m][p]: the sum of the squares of a share of matrix m, in 64 bits (no square of an fp32 value leaves them).
 template <int DT>
 __global__ __launch_bounds__(kNormThreads) void orth_norm_kernel(const void *__restrict__ g, int64_t size, int parts,
                                                                  double *__restrict__ part) {
     const int m = blockIdx.x / parts, p = blockIdx.x % parts;
-    const int64_t from = size * p / parts, to = size * (p + 1) / parts;
+    const int64_t eights = (size + 7) / 8, from = eights * p / parts, to = eights * (p + 1) / parts;
     double sum = 0.0;
     for (int64_t i = from + threadIdx.x; i < to; i += kNormThreads) {
-        const double v = load_value<DT>(g, m * size + i);
-        sum += v * v;
+        float v[8];
+        load8<DT>(g, m * size + i * 8, size - i * 8, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum += (double)v[k] * v[k];
     }
     __shared__ double all[kNormThreads];
     all[threadIdx.x] = sum;
@@ -58,33 +55,66 @@ __global__ __launch_bounds__(kNormThreads) void orth_norm_kernel(const void *__r
     if (threadIdx.x == 0) part[blockIdx.x] = all[0];
 }
 
-// X_0 in pairs: a workgroup takes 32 x 32 values, of G^T where `tall`.
-template <int DT>
-__global__ __launch_bounds__(256) void orth_first_kernel(const void *__restrict__ g, const double *__restrict__ part,
-                                                         int parts, double eps, int tall, int r, int c, int rp, int cp,
-                                                         uint16_t *__restrict__ x) {
-    const int m = blockIdx.z, c0 = blockIdx.x * 32, r0 = blockIdx.y * 32;
-    double sum = 0.0;
-    for (int p = 0; p < parts; ++p) sum += part[m * parts + p];
-    const double inv = 1.0 / (sqrt(sum) + eps);
-    __shared__ float v[32][33];
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+// 1 / (norm + eps) of matrix m from its at most 64 parts, in every lane.
+__device__ __forceinline__ double orth_inverse(const double *part, int m, int parts, double eps) {
+    const int lane = threadIdx.x & 63;
+    double sum = lane < parts ? part[m * (int64_t)parts + lane] : 0.0;
 #pragma unroll
-    for (int k = 0; k < 32; k += 8) {
-        // (row, column) of X; lanes run along G's rows
-        const int i = tall ? r0 + tx : r0 + ty + k, j = tall ? c0 + ty + k : c0 + tx;
-        const int64_t at = (int64_t)m * r * c + (tall ? (int64_t)j * r + i : (int64_t)i * c + j);
-        v[i - r0][j - c0] = i < r && j < c ? (float)((double)load_value<DT>(g, at) * inv) : 0.0f;
+    for (int w = 32; w >= 1; w >>= 1) sum += __shfl_xor(sum, w, 64);
+    return 1.0 / (sqrt(sum) + eps);
+}
+
+// Eight values of a row of X as pairs: `at` is a multiple of 8.
+__device__ __forceinline__ void store_pairs(uint16_t *row, int at, const float (&v)[8]) {
+    u32x4 oh, ol;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float hi[2], lo[2];
+        split_pair(v[2 * k], hi[0], lo[0]);
+        split_pair(v[2 * k + 1], hi[1], lo[1]);
+        oh[k] = pack_bf16x2(hi[0], hi[1]);
+        ol[k] = pack_bf16x2(lo[0], lo[1]);
     }
-    __syncthreads();
+    uint16_t *to = row + (at >> 5) * 64 + (at & 31);
+    *(u32x4 *)to = oh;
+    *(u32x4 *)(to + 32) = ol;
+}
+
+// X_0 in pairs.  A workgroup takes 64 x 64 values; those of G^T (TALL) are turned over in LDS.
+template <int DT, bool TALL>
+__global__ __launch_bounds__(256) void orth_first_kernel(const void *__restrict__ g, const double *__restrict__ part,
+                                                         int parts, double eps, int r, int c, int rp, int cp,
+                                                         uint16_t *__restrict__ x) {
+    const int m = blockIdx.z, c0 = blockIdx.x * 64, r0 = blockIdx.y * 64;
+    const double inv = orth_inverse(part, m, parts, eps);
+    const int64_t base = (int64_t)m * r * c;
+    __shared__ float turned[TALL ? 64 * 65 : 1];
+    const int row = threadIdx.x >> 3, eight = (threadIdx.x & 7) * 8;
+    if (TALL) {
+        // rows of G are columns of X
 #pragma unroll
-    for (int k = 0; k < 32; k += 8) {
-        const int i = r0 + ty + k;
-        float hi, lo;
-        split_pair(v[ty + k][tx], hi, lo);
-        uint16_t *row = x + ((int64_t)m * rp + i) * cp * 2 + c0 * 2;
-        row[tx] = (uint16_t)pack_bf16x2(hi, 0.0f);
-        row[32 + tx] = (uint16_t)pack_bf16x2(lo, 0.0f);
+        for (int k = 0; k < 64; k += 32) {
+            const int j = c0 + row + k, i = r0 + eight;
+            float v[8];
+            load8<DT>(g, base + (int64_t)j * r + i, j < c ? r - i : 0, v);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) turned[(eight + q) * 65 + row + k] = v[q];
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < 64; k += 32) {
+        const int i = r0 + row + k, j = c0 + eight;
+        float v[8];
+        if (TALL) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = turned[(row + k) * 65 + eight + q];
+        } else {
+            load8<DT>(g, base + (int64_t)i * c + j, i < r ? c - j : 0, v);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = (float)((double)v[q] * inv);
+        if (i < rp && j < cp) store_pairs(x + ((int64_t)m * rp + i) * cp * 2, j, v);
     }
 }
 
@@ -126,6 +156,7 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
     extern __shared__ __align__(1024) char smem[];
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     char *const ring = smem;
+    const int filled = lds_place(ring);              // the ring for direct loads
     uint32_t *const turn = (uint32_t *)(smem + SLOTS * STAGE) + wid * (16 * 17);
     const int at = (a.A + T::TA - 1) / T::TA, bt = (a.B + T::TB - 1) / T::TB;
     // symmetric: the tiles that reach the diagonal or lie below it (b >= a), for each column of tiles a run of them
@@ -139,7 +170,7 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
     const int per = (total + 7) / 8, xcd = blockIdx.x & 7;
     const int end = min(total, (xcd + 1) * per), first = xcd * per + (blockIdx.x >> 3), step = gridDim.x >> 3;
     if (first >= end) return;
-    auto find = [&](int t, int &m, int &a0, int &b0) {
+    auto find = [&](int t, int &m, int &a0, int &b0) __attribute__((always_inline)) {
         m = __builtin_amdgcn_readfirstlane(t / per_matrix);
         int rest = t - m * per_matrix, ia = 0;
         if (SYM) {
@@ -158,16 +189,16 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
 
     // ---- loads ----
     int it = first, ik = 0;
-    __amdgpu_buffer_rsrc_t ar, br;
+    i32x4s ar, br;
     uint32_t avoff[RB], bvoff[QB];
     const int a_step = ASTRIDED ? 32 * a.A * 4 : 128;
     auto bytes_at = [&](int row) { return ((lane & 7) ^ swz<128>(row)) << 4; };
-    auto aim = [&]() {
+    auto aim = [&]() __attribute__((always_inline)) {
         int m, a0, b0;
         find(it, m, a0, b0);
         const int64_t amat = (int64_t)(ASTRIDED ? a.K : a.A) * (ASTRIDED ? a.A : a.K) * 2, bmat = (int64_t)a.B * a.K * 2;
-        ar = buffer_of(a.a + m * amat, amat * 2);
-        br = buffer_of(a.b + m * bmat, bmat * 2);
+        ar = words_of(a.a + m * amat, amat * 2);
+        br = words_of(a.b + m * bmat, bmat * 2);
 #pragma unroll
         for (int q = 0; q < RB; ++q) {
             if (ASTRIDED) {
@@ -188,14 +219,14 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
         }
     };
     // issues a step's N loads; 0 behind the last tile
-    auto issue = [&](int slot) {
+    auto issue = [&](int slot) __attribute__((always_inline)) {
         if (it >= end) return 0;
         if (ik == 0) aim();
-        char *as = ring + slot * STAGE + wid * (RB * 1024), *bs = ring + slot * STAGE + T::stage_a + wid * 1024;
+        const int as = filled + slot * STAGE + wid * (RB * 1024), bs = filled + slot * STAGE + T::stage_a + wid * 1024;
 #pragma unroll
-        for (int q = 0; q < RB; ++q) buffer_dma16(ar, avoff[q], ik * a_step, as + q * 1024);
+        for (int q = 0; q < RB; ++q) fill16(ar, avoff[q], ik * a_step, as + q * 1024);
 #pragma unroll
-        for (int q = 0; q < QB; ++q) buffer_dma16(br, bvoff[q], ik * 128, bs + q * 8192);
+        for (int q = 0; q < QB; ++q) fill16(br, bvoff[q], ik * 128, bs + q * 8192);
         if (++ik == steps) {
             ik = 0;
             it += step;
@@ -367,7 +398,7 @@ OrthSizes orth_sizes(int64_t n, int64_t rows, int64_t cols) {
     z.c = z.tall ? rows : cols;
     z.rp = (z.r + 31) / 32 * 32;
     z.cp = (z.c + 31) / 32 * 32;
-    z.parts = (int)(z.r * z.c / 65536 + 1 < 64 ? z.r * z.c / 65536 + 1 : 64);
+    z.parts = (int)(z.r * z.c / 16384 + 1 < 64 ? z.r * z.c / 16384 + 1 : 64);
     z.x = (size_t)n * z.rp * z.cp * 4;
     z.s = (size_t)n * z.rp * z.rp * 4;
     z.norm = ((size_t)n * z.parts * 8 + 255) / 256 * 256;
@@ -386,14 +417,15 @@ hipError_t launch_orthogonalize(const OrthProblem &q, hipStream_t s) {
     gram = take(z.s);
     poly = take(z.s);
     const int n = (int)q.n, r = (int)z.r, c = (int)z.c, rp = (int)z.rp, cp = (int)z.cp;
-    const dim3 blocks(cp / 32, rp / 32, n);
-    if (q.dt == DT_F32) {
-        orth_norm_kernel<DT_F32><<<n * z.parts, kNormThreads, 0, s>>>(q.g, z.r * z.c, z.parts, part);
-        orth_first_kernel<DT_F32><<<blocks, 256, 0, s>>>(q.g, part, z.parts, q.eps, z.tall, r, c, rp, cp, x[0]);
-    } else {
-        orth_norm_kernel<DT_BF16><<<n * z.parts, kNormThreads, 0, s>>>(q.g, z.r * z.c, z.parts, part);
-        orth_first_kernel<DT_BF16><<<blocks, 256, 0, s>>>(q.g, part, z.parts, q.eps, z.tall, r, c, rp, cp, x[0]);
-    }
+    const dim3 blocks((cp + 63) / 64, (rp + 63) / 64, n);
+    auto first = [&](auto dtc) {
+        constexpr int D = decltype(dtc)::value;
+        orth_norm_kernel<D><<<n * z.parts, kNormThreads, 0, s>>>(q.g, z.r * z.c, z.parts, part);
+        if (z.tall) orth_first_kernel<D, true><<<blocks, 256, 0, s>>>(q.g, part, z.parts, q.eps, r, c, rp, cp, x[0]);
+        else orth_first_kernel<D, false><<<blocks, 256, 0, s>>>(q.g, part, z.parts, q.eps, r, c, rp, cp, x[0]);
+    };
+    if (q.dt == DT_F32) first(std::integral_constant<int, DT_F32>{});
+    else first(std::integral_constant<int, DT_BF16>{});
     hipError_t e = hipGetLastError();
     for (int k = 0; k < q.steps && e == hipSuccess; ++k) {
         const float *co = q.coeffs + 3 * k;

@@ -57,7 +57,6 @@ struct Product<DT_I8> {
 __device__ const u32x4 product_zeros = {0, 0, 0, 0};
 
 // Values e0 .. e0 + 7 of a bf16 row of `n` values at any address, zeros past its end.
-typedef u32x4 u32x4_any __attribute__((aligned(2)));
 __device__ __forceinline__ u32x4 row_chunk(const uint16_t *row, int64_t e0, int64_t n) {
     if (e0 + 8 <= n) return *(const u32x4_any *)(row + e0);
     u32x4 v = {0, 0, 0, 0};
@@ -67,16 +66,83 @@ __device__ __forceinline__ u32x4 row_chunk(const uint16_t *row, int64_t e0, int6
     return v;
 }
 
+// Writes a wave's results: 16-value blocks of a from f0 on, 16-row blocks of b in turn with the other wave's.
+template <int DT, int RB, int TB, bool DW, class Acc>
+__device__ __forceinline__ void product_store(const ProductPass &a, const Acc (&acc)[RB][TB], int e, int f0, int row0,
+                                              int valid, int wb, int lane) {
+    const int r15 = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+        const int b = (j * 2 + wb) * 16 + r15;
+        const bool there = b < valid;
+        float v[RB][4];
+        float sb = 1.0f;
+        if constexpr (DT == DT_I8) {
+            const int64_t R = row0 + min(b, valid - 1);
+            sb = a.sb[a.gather ? (int64_t)a.gather[R] : R];
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (DT == DT_I8) {
+                    const int f = f0 + i * 16 + 4 * g + q;
+                    v[i][q] = (float)acc[i][j][q] * sb * a.sa[(int64_t)e * a.A + min(f, a.A - 1)];
+                } else {
+                    v[i][q] = acc[i][j][q];
+                }
+            }
+        const int64_t at = (DW ? ((int64_t)e * a.B + row0 + b) : (int64_t)row0 + b) * a.out_ld;
+        if (a.out_f32) {
+            float *row = (float *)a.out + at;
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                const int f = f0 + i * 16 + 4 * g;
+                if (!there) continue;
+                if (a.wide && f < a.A) {
+                    f32x4 o = {v[i][0], v[i][1], v[i][2], v[i][3]};
+                    if (a.accumulate) o += *(const f32x4 *)(row + f);
+                    *(f32x4 *)(row + f) = o;
+                } else if (!a.wide) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (f + q < a.A) row[f + q] = v[i][q] + (a.accumulate ? row[f + q] : 0.0f);
+                }
+            }
+        } else {
+            uint16_t *row = (uint16_t *)a.out + at;
+#pragma unroll
+            for (int i = 0; i < RB; i += 2) {
+                if (a.wide) {
+                    const u32x4 o = pair_bf16_value(v[i], v[i + 1], lane);
+                    const int f = pair_bf16_col(f0 + i * 16, lane);
+                    if (there && f < a.A) *(u32x4 *)(row + f) = o;
+                } else if (there) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int f = f0 + (i + h) * 16 + 4 * g + q;
+                            if (f < a.A) row[f] = (uint16_t)pack_bf16x2(v[i + h][q], 0.0f);
+                        }
+                }
+            }
+        }
+    }
+}
+
 template <int DT, int OP, int CAP, bool DIRECT>
 __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const ProductPass a) {
     typedef Product<DT> P;
     constexpr int esz = P::esz, SLOTS = DIRECT ? product_slots<CAP>() : 2, STAGE = product_stage<CAP>();
     constexpr bool DW = OP == PRODUCT_DW, ASTRIDED = OP != PRODUCT_Y;
+    static_assert(!DW || !DIRECT, "product_dw_kernel");
     constexpr int QB = CAP / 2 + CAP % 2;            // loads of B a wave issues for a step, at most
     extern __shared__ __align__(1024) char smem[];
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     int32_t *const ends = (int32_t *)smem;
     char *const ring = smem + kEndBytes;
+    const int filled = lds_place(ring);              // the ring for direct loads
     for (int i = tid; i < a.n_exp; i += kProductThreads)
         ends[i] = (int)max((int64_t)0, min((int64_t)a.offsets[i + 1], a.max_rows));
     __syncthreads();
@@ -97,7 +163,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
     if (first >= end) return;
 
     // tile t: expert, first value of a, first row (of the rows, or of dw's features) and their number
-    auto find = [&](int t, int &e, int &a0, int &row0, int &valid) {
+    auto find = [&](int t, int &e, int &a0, int &row0, int &valid) __attribute__((always_inline)) {
         if (DW) {
             e = t / (atiles * btiles);
             const int rest = t - e * (atiles * btiles), bt = rest / atiles;
@@ -114,11 +180,11 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
     auto first_of = [&](int e) { return __builtin_amdgcn_readfirstlane(list.start(e)); };
     auto rows_of = [&](int e) { return __builtin_amdgcn_readfirstlane(ends[e]) - first_of(e); };
     constexpr int KSTEP = 128 / esz;                  // of the reduction
-    auto steps_of = [&](int e) { return DW ? max(1, (rows_of(e) + KSTEP - 1) / KSTEP) : (a.K + KSTEP - 1) / KSTEP; };
+    auto steps_of = [&](int e) __attribute__((always_inline)) { return DW ? max(1, (rows_of(e) + KSTEP - 1) / KSTEP) : (a.K + KSTEP - 1) / KSTEP; };
 
     // ---- loads: the tile and step that come next ----
     int it = first, ik = 0, isteps = 0, ie = 0, ia0 = 0, irow0 = 0, ivalid = 0;
-    __amdgpu_buffer_rsrc_t ar;
+    i32x4s ar;
     uint32_t avoff[4];
     const char *bptr[QB];
     // places in a stage: A's load q of the wave brings 1 KB to (wid * 4 + q) * 1024, B's to (q * 8 + wid) * 1024
@@ -126,7 +192,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
     const int ak0 = wid * 8 + (lane >> 5);            // rows of the reduction
     auto bytes_at = [&](int row) { return ((lane & 7) ^ swz<128>(row)) << 4; };           // within 128 bytes of a row
     auto values_at = [&](int k) { return ((lane & 31) ^ strided_slot(k)) * 8; };           // within 256 values
-    auto aim = [&]() {
+    auto aim = [&]() __attribute__((always_inline)) {
         find(it, ie, ia0, irow0, ivalid);
         isteps = steps_of(ie);
         if (!DW) {
@@ -134,9 +200,9 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
             const int n = min(kTileA, a.A - ia0);
             if (!ASTRIDED) {
                 base += (int64_t)ia0 * a.a_ld * esz;
-                ar = buffer_of(base, (int64_t)n * a.a_ld * esz);
+                ar = words_of(base, (int64_t)n * a.a_ld * esz);
             } else {
-                ar = buffer_of(base, a.a_mat * esz);
+                ar = words_of(base, a.a_mat * esz);
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -155,11 +221,12 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
                 const int64_t R = irow0 + min(row, ivalid - 1);
                 const int64_t token = a.gather ? (int64_t)a.gather[R] : R;
                 bptr[q] = (const char *)a.b + token * a.b_ld * esz + bytes_at(row);
+                arrived(bptr[q]);
             }
         }
     };
     // A strided operand's 16 bytes of load q in step k (dw): row r of the reduction, values c .. c + 7
-    auto dw_chunk = [&](int q, bool isA, const uint16_t *&row, int &c) {
+    auto dw_chunk = [&](int q, bool isA, const uint16_t *&row, int &c) __attribute__((always_inline)) {
         const int k = ak0 + q * 2, r = ik * 64 + k, m = rows_of(ie);
         const int64_t R = first_of(ie) + min(r, max(m - 1, 0));
         c = (isA ? ia0 : irow0) + values_at(k);
@@ -171,34 +238,22 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
     };
     const int64_t kbytes = (int64_t)a.K * esz;
     // issues a step's loads into a stage; the number of loads
-    auto issue = [&](char *stage) {
+    auto issue = [&](int stage) __attribute__((always_inline)) {
         if (it >= end) return 0;
         if (ik == 0) aim();
-        char *as = stage + wid * 4096, *bs = stage + kProductStageA + wid * 1024;
+        const int as = stage + wid * 4096, bs = stage + kProductStageA + wid * 1024;
         int n = 4;
-        if constexpr (DW) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint16_t *row;
-                int c;
-                dw_chunk(q, true, row, c);
-                dma16(row ? (const void *)(row + c) : (const void *)&product_zeros, as + q * 1024);
-                dw_chunk(q, false, row, c);
-                dma16(row ? (const void *)(row + c) : (const void *)&product_zeros,
-                      stage + kProductStageA + wid * 4096 + q * 1024);
-            }
-            n = 8;
-        } else {
+        if constexpr (!DW) {
             const bool tail = ik == isteps - 1;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint32_t vo = avoff[q];
                 if (!ASTRIDED) {
                     if (tail && (int64_t)ik * 128 + bytes_at(arow0 + q * 8) >= kbytes) vo = kNoOffset;
-                    buffer_dma16(ar, vo, ik * 128, as + q * 1024);
+                    fill16(ar, vo, ik * 128, as + q * 1024);
                 } else {
                     if (tail && ik * 64 + ak0 + q * 2 >= a.K) vo = kNoOffset;
-                    buffer_dma16(ar, vo, (int)(ik * 64 * a.a_ld * esz), as + q * 1024);
+                    fill16(ar, vo, (int)(ik * 64 * a.a_ld * esz), as + q * 1024);
                 }
             }
             const int blocks = (ivalid + 31) >> 5;
@@ -208,7 +263,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
                     const int at = bytes_at((q * 8 + wid) * 8 + (lane >> 3));
                     const void *src = bptr[q] + (int64_t)ik * 128;
                     if (tail && (int64_t)ik * 128 + at >= kbytes) src = &product_zeros;
-                    dma16(src, bs + q * 8192);
+                    fill16(src, bs + q * 8192);
                     ++n;
                 }
         }
@@ -221,7 +276,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
     // the same through registers, for rows that do not lie at multiples of 16 bytes
     u32x4 areg[4], breg[DW ? 4 : QB];
     int iblocks = 0;
-    auto fetch = [&]() {
+    auto fetch = [&]() __attribute__((always_inline)) {
         iblocks = 0;
         if (it >= end) return;
         if (ik == 0) aim();
@@ -264,7 +319,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
             it += step;
         }
     };
-    auto put = [&](char *stage) {
+    auto put = [&](char *stage) __attribute__((always_inline)) {
         if (!iblocks) return;
         char *as = stage + wid * 4096 + lane * 16, *bs = stage + kProductStageA + lane * 16;
 #pragma unroll
@@ -296,7 +351,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
     }
     int slot = 0, n1 = 0;
     auto next = [](int s) { return s + 1 == SLOTS ? 0 : s + 1; };
-    auto tile = [&](auto tbc, int steps, int e, int a0, int row0, int valid) {
+    auto tile = [&](auto tbc, int steps, int e, int a0, int row0, int valid) __attribute__((always_inline)) {
         constexpr int TB = decltype(tbc)::value;
         typename P::acc acc[4][TB] = {};
         for (int k = 0; k < steps; ++k) {
@@ -308,7 +363,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
             }
             wait_lgkm0();
             cta_barrier();
-            if (DIRECT) n1 = issue(ring + (SLOTS == 3 ? next(next(slot)) : next(slot)) * STAGE);
+            if (DIRECT) n1 = issue(filled + (SLOTS == 3 ? next(next(slot)) : next(slot)) * STAGE);
             else fetch();
             const char *as = ring + slot * STAGE, *bs = as + kProductStageA;
 #pragma unroll
@@ -333,70 +388,11 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
             if (!DIRECT) put(ring + next(slot) * STAGE);
             slot = next(slot);
         }
-        // ---- results ----
-        const int f0 = a0 + wf * 64;
-#pragma unroll
-        for (int j = 0; j < TB; ++j) {
-            const int b = (j * 2 + wm) * 16 + r15;
-            const bool there = b < valid;
-            float v[4][4];
-            float sb = 1.0f;
-            if constexpr (DT == DT_I8) {
-                const int64_t R = row0 + min(b, valid - 1);
-                sb = a.sb[a.gather ? (int64_t)a.gather[R] : R];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if constexpr (DT == DT_I8) {
-                        const int f = f0 + i * 16 + 4 * g + q;
-                        v[i][q] = (float)acc[i][j][q] * sb * a.sa[(int64_t)e * a.A + min(f, a.A - 1)];
-                    } else {
-                        v[i][q] = acc[i][j][q];
-                    }
-                }
-            const int64_t at = (DW ? ((int64_t)e * a.B + row0 + b) : (int64_t)row0 + b) * a.out_ld;
-            if (a.out_f32) {
-                float *row = (float *)a.out + at;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int f = f0 + i * 16 + 4 * g;
-                    if (!there) continue;
-                    if (a.wide && f < a.A) {
-                        f32x4 o = {v[i][0], v[i][1], v[i][2], v[i][3]};
-                        if (a.accumulate) o += *(const f32x4 *)(row + f);
-                        *(f32x4 *)(row + f) = o;
-                    } else if (!a.wide) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (f + q < a.A) row[f + q] = v[i][q] + (a.accumulate ? row[f + q] : 0.0f);
-                    }
-                }
-            } else {
-                uint16_t *row = (uint16_t *)a.out + at;
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    if (a.wide) {
-                        const u32x4 o = pair_bf16_value(v[i], v[i + 1], lane);
-                        const int f = pair_bf16_col(f0 + i * 16, lane);
-                        if (there && f < a.A) *(u32x4 *)(row + f) = o;
-                    } else if (there) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const int f = f0 + (i + h) * 16 + 4 * g + q;
-                                if (f < a.A) row[f] = (uint16_t)pack_bf16x2(v[i + h][q], 0.0f);
-                            }
-                    }
-                }
-            }
-        }
+        product_store<DT, 4, TB, DW>(a, acc, e, a0 + wf * 64, row0, valid, wm, lane);
     };
     if (DIRECT) {
-        issue(ring);
-        if (SLOTS == 3) n1 = issue(ring + STAGE);
+        issue(filled);
+        if (SLOTS == 3) n1 = issue(filled + STAGE);
     } else {
         fetch();
         put(ring);
@@ -422,79 +418,435 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
     }
 }
 
+// dw for operands and results at multiples of 16 bytes.  A tile is 256 inputs by 256 features of one expert; the expert's rows are
+// taken 32 at a time through a ring of four stages, of which three are under way (with two stages of 64 rows, whose gather
+// indexes were vector loads that every load under way had to end for, 32 experts of 512 rows took 1165 us).  The rows' indexes come
+// by scalar loads a stage ahead.  Results leave by stores without branches, so that their number is known: a stage's loads
+// are waited for by counting what was issued behind them, and the stores of one tile drain under the next.  Tiles are listed in
+// groups of 8 along a, so that the 32 of an XCD share 8 blocks of x and 4 of dy.
+constexpr int kDwStage = 2 * 32 * 512;
+constexpr int kDwSlots = 4;
+constexpr int kDwLds = kEndBytes + kDwSlots * kDwStage;
+
+__global__ __launch_bounds__(kProductThreads, 1) void product_dw_kernel(const ProductPass a) {
+    extern __shared__ __align__(1024) char smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int32_t *const ends = (int32_t *)smem;
+    const char *const ring = smem + kEndBytes;
+    const int filled = lds_place(ring);              // the ring for direct loads
+    for (int i = tid; i < a.n_exp; i += kProductThreads)
+        ends[i] = (int)max((int64_t)0, min((int64_t)a.offsets[i + 1], a.max_rows));
+    __syncthreads();
+    const int atiles = (a.A + 255) / 256, btiles = (a.B + 255) / 256, total = a.n_exp * atiles * btiles;
+    // workgroup b runs on XCD b mod 8: each XCD takes a contiguous eighth of the list
+    const int per = (total + 7) / 8, xcd = blockIdx.x & 7;
+    const int end = min(total, (xcd + 1) * per), first = xcd * per + (blockIdx.x >> 3), step = gridDim.x >> 3;
+    if (first >= end) return;
+    auto find = [&](int t, int &e, int &a0, int &b0) __attribute__((always_inline)) {
+        e = __builtin_amdgcn_readfirstlane(t / (atiles * btiles));
+        const int rest = t - e * (atiles * btiles), group = __builtin_amdgcn_readfirstlane(rest / (8 * btiles));
+        const int in = rest - group * (8 * btiles), wide = min(8, atiles - group * 8);
+        const int bt = __builtin_amdgcn_readfirstlane(in / wide);
+        a0 = (group * 8 + in - bt * wide) * 256;
+        b0 = bt * 256;
+    };
+    auto start_of = [&](int e) { return e ? __builtin_amdgcn_readfirstlane(ends[e - 1]) : 0; };
+    auto rows_of = [&](int e) { return max(0, __builtin_amdgcn_readfirstlane(ends[e]) - start_of(e)); };
+    // an expert without rows takes one step of zeros
+    auto steps_of = [&](int rows) { return max(1, (rows + 31) / 32); };
+
+    // ---- loads: the tile and step that come next, and the rows of x that this wave's loads of it bring ----
+    const int k0 = wid * 4 + (lane >> 5);             // the lane's row of a step, in load 0; load 1 is two on
+    int it = first, ik = 0, isteps = 0, lo = 0, rows = 0, index[4] = {0, 0, 0, 0};
+    int64_t aoff[2], boff[2];                         // bytes within rows; -1: past the row's values
+    auto look = [&]() __attribute__((always_inline)) {
+        if (it >= end) return;
+        if (ik == 0) {
+            int e, a0, b0;
+            find(it, e, a0, b0);
+            lo = start_of(e);
+            rows = rows_of(e);
+            isteps = steps_of(rows);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int c = ((lane & 31) ^ strided_slot(k0 + q * 2)) * 8;
+                aoff[q] = a0 + c < a.A ? (a0 + c) * 2ll : -1;
+                boff[q] = b0 + c < a.B ? (b0 + c) * 2ll : -1;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = lo + min(ik * 32 + wid * 4 + i, rows - 1);
+            index[i] = rows > 0 && a.gather ? scalar_load(a.gather, r) : r;
+        }
+    };
+    int ops = 0;                                      // vector memory instructions so far
+    auto issue = [&](int stage) __attribute__((always_inline)) {
+        if (it >= end) return;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int r = ik * 32 + k0 + q * 2;
+            const bool there = r < rows;
+            const int64_t xrow = lane >> 5 ? index[q * 2 + 1] : index[q * 2];
+            const char *x = (const char *)a.a + xrow * a.a_ld * 2 + aoff[q];
+            const char *y = (const char *)a.b + (int64_t)(lo + r) * a.b_ld * 2 + boff[q];
+            fill16(there && aoff[q] >= 0 ? x : (const char *)&product_zeros, stage + wid * 2048 + q * 1024);
+            fill16(there && boff[q] >= 0 ? y : (const char *)&product_zeros, stage + kDwStage / 2 + wid * 2048 + q * 1024);
+        }
+        ops += 4;
+        if (++ik == isteps) {
+            ik = 0;
+            it += step;
+        }
+        look();
+    };
+
+    const int wf = wid >> 1, wm = wid & 1, r15 = lane & 15, g = lane >> 4;
+    int aofs[4], bofs[4];
+    {
+        const int jj = (lane >> 2) & 3, aa = lane & 3, k = 8 * g + jj;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int ca = wf * 8 + i * 2 + (aa >> 1), cb = i * 4 + wm * 2 + (aa >> 1);
+            aofs[i] = k * 512 + ((ca ^ strided_slot(k)) << 4) + 8 * (aa & 1);
+            bofs[i] = k * 512 + ((cb ^ strided_slot(k)) << 4) + 8 * (aa & 1) + kDwStage / 2;
+        }
+    }
+    look();
+    int slot = 0, mark[kDwSlots - 1];                 // `ops` behind the loads of the steps that come
+#pragma unroll
+    for (int i = 0; i < kDwSlots - 1; ++i) {
+        issue(filled + i * kDwStage);
+        mark[i] = ops;
+    }
+    for (int t = first; t < end; t += step) {
+        int e, a0, b0;
+        find(t, e, a0, b0);
+        const int steps = steps_of(rows_of(e));
+        f32x4 acc[4][8] = {};
+        for (int k = 0; k < steps; ++k) {
+            wait_vmcnt_dyn(ops - mark[0]);
+            wait_lgkm0();
+            cta_barrier();
+            // past the barrier every wave's loads of the stage are done, and the stage before has been read
+            issue(filled + ((slot + kDwSlots - 1) & (kDwSlots - 1)) * kDwStage);
+            mark[0] = mark[1];
+            mark[1] = mark[2];
+            mark[2] = ops;
+            const char *st = ring + slot * kDwStage;
+            bf16x8 af[4], bf[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) af[i] = read_strided<512>(st + aofs[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) bf[j] = read_strided<512>(st + bofs[j & 3] + (j >> 2) * 256);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i][j] = Product<DT_BF16>::mma(af[i], bf[j], acc[i][j]);
+            slot = (slot + 1) & (kDwSlots - 1);
+        }
+        const int f0 = a0 + wf * 64, osz = a.out_f32 ? 4 : 2, valid = min(256, a.B - b0);
+        const __amdgpu_buffer_rsrc_t out =
+            buffer_of((const char *)a.out + ((int64_t)e * a.B + b0) * a.A * osz, (int64_t)valid * a.A * osz);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int b = (j * 2 + wm) * 16 + r15;
+            const uint32_t row = b < valid ? (uint32_t)(b * a.A * osz) : kNoOffset;
+            if (a.out_f32) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int f = f0 + i * 16 + 4 * g;
+                    const uint32_t at = f < a.A ? row + f * 4 : kNoOffset;
+                    f32x4 v = acc[i][j];
+                    if (a.accumulate) v += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(out, at, 0, 0));
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), out, at, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const float va[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                    const float vb[4] = {acc[i + 1][j][0], acc[i + 1][j][1], acc[i + 1][j][2], acc[i + 1][j][3]};
+                    const int f = pair_bf16_col(f0 + i * 16, lane);
+                    __builtin_amdgcn_raw_buffer_store_b128(pair_bf16_value(va, vb, lane), out,
+                                                           f < a.A ? row + f * 2 : kNoOffset, 0, 0);
+                }
+            }
+        }
+        ops += a.out_f32 ? 32 : 16;
+    }
+}
+
+// Few tiles: a single token to its experts, small matrices.  Bound by the time from one load to the next, so the work is cut
+// finely: a tile is 64 values of a by up to 8 rows of b, and the four waves of a workgroup share it, each a quarter of the steps,
+// which pass through a ring in LDS of the wave's own without barriers.  The sums meet in LDS, in the order of the waves.
+// One token, 8 experts of 7168 x 2048 (235 MB): 50 us against 69 in tiles of 256.
+constexpr int kStreamThreads = 256;
+constexpr int kStreamRows = product_rows(kProductStream);
+constexpr int kStreamStageA = 64 * 128, kStreamStage = kStreamStageA + kStreamRows * 128, kStreamSlots = 4;
+constexpr int kStreamParts = 3 * 4 * 64 * 16;
+constexpr int kStreamLds = kEndBytes + 4 * kStreamSlots * kStreamStage + kStreamParts;
+static_assert(kStreamLds <= 160 * 1024, "LDS");
+
+// rows of 128 bytes: as strided_slot, with the row's lowest bit in the place of the 128
+__device__ __forceinline__ int stream_slot(int k) { return 2 * (((k >> 1) & 1) | (((k >> 3) & 1) << 1)); }
+
+template <int DT, bool ASTRIDED>
+__global__ __launch_bounds__(kStreamThreads, 1) void product_stream_kernel(const ProductPass a) {
+    typedef Product<DT> P;
+    typedef typename P::frag frag;
+    constexpr int esz = P::esz;
+    extern __shared__ __align__(1024) char smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int32_t *const ends = (int32_t *)smem;
+    const char *const ring = smem + kEndBytes + wid * (kStreamSlots * kStreamStage);
+    const int filled = lds_place(ring);
+    u32x4 *const parts = (u32x4 *)(smem + kEndBytes + 4 * kStreamSlots * kStreamStage);
+    for (int i = tid; i < a.n_exp; i += kStreamThreads)
+        ends[i] = (int)max((int64_t)0, min((int64_t)a.offsets[i + 1], a.max_rows));
+    __syncthreads();
+    TileList list;
+    list.init(ends, a.n_exp, kStreamRows, (a.A + 63) / 64, lane);
+    const int steps = (int)(((int64_t)a.K * esz + 127) / 128), part = (int)((int64_t)a.K * esz % 128);
+    const int klo = steps * wid / 4, khi = steps * (wid + 1) / 4;
+
+    // ---- loads: the tile and step that come next ----
+    int it = blockIdx.x, ik = klo;
+    i32x4s ar = {};
+    uint32_t avoff[8];
+    const char *brow = nullptr;
+    const int piece = ((lane & 7) ^ swz<128>(lane >> 3)) << 4;
+    int ops = 0;
+    auto issue = [&](int stage) __attribute__((always_inline)) {
+        if (it >= list.total || klo >= khi) return;
+        if (ik == klo) {
+            int e, ft, row0, valid;
+            list.find(it, lane, e, ft, row0, valid);
+            const int a0 = ft * 64;
+            const char *base = (const char *)a.a + (int64_t)e * a.a_mat * esz;
+            if (!ASTRIDED) ar = words_of(base + (int64_t)a0 * a.a_ld * esz, (int64_t)min(64, a.A - a0) * a.a_ld * esz);
+            else ar = words_of(base, a.a_mat * esz);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int row = q * 8 + (lane >> 3);
+                if (!ASTRIDED) {
+                    avoff[q] = a0 + row < a.A ? (uint32_t)((int64_t)row * a.a_ld * esz) + piece : kNoOffset;
+                } else {
+                    const int c = a0 + ((lane & 7) ^ stream_slot(row)) * 8;
+                    avoff[q] = c < a.A ? (uint32_t)(((int64_t)row * a.a_ld + c) * esz) : kNoOffset;
+                }
+            }
+            // rows past the tile's repeat its last one; their results are not used
+            int token = row0 + min(lane >> 3, valid - 1);
+            if (a.gather) token = a.gather[token];
+            brow = (const char *)a.b + (int64_t)token * a.b_ld * esz + piece;
+            arrived(brow);
+        }
+        const bool tail = part && ik == steps - 1;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            uint32_t vo = avoff[q];
+            if (!ASTRIDED) {
+                if (tail) vo = piece >= part ? kNoOffset : vo;
+                fill16(ar, vo, ik * 128, stage + q * 1024);
+            } else {
+                if (tail) vo = ik * 64 + q * 8 + (lane >> 3) >= a.K ? kNoOffset : vo;
+                fill16(ar, vo, (int)(ik * 64 * a.a_ld * esz), stage + q * 1024);
+            }
+        }
+        const char *src = brow + (int64_t)ik * 128;
+        if (tail) src = piece >= part ? (const char *)&product_zeros : src;
+        fill16(src, stage + kStreamStageA);
+        ops += 9;
+        if (++ik == khi) {
+            ik = klo;
+            it += gridDim.x;
+        }
+    };
+
+    const int r15 = lane & 15, g = lane >> 4, row8 = r15 & (kStreamRows - 1);
+    const int alo = r15 * 128 + ((g ^ swz<128>(r15)) << 4), blo = kStreamStageA + row8 * 128 + ((g ^ swz<128>(row8)) << 4);
+    int aofs[4];
+    {
+        const int jj = (lane >> 2) & 3, aa = lane & 3, k = 8 * g + jj;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) aofs[i] = k * 128 + (((i * 2 + (aa >> 1)) ^ stream_slot(k)) << 4) + 8 * (aa & 1);
+    }
+    int slot = 0, mark[kStreamSlots - 1];
+#pragma unroll
+    for (int i = 0; i < kStreamSlots - 1; ++i) {
+        issue(filled + i * kStreamStage);
+        mark[i] = ops;
+    }
+    for (int t = blockIdx.x; t < list.total; t += gridDim.x) {
+        typename P::acc acc[4][1] = {};
+        for (int k = klo; k < khi; ++k) {
+            // the step's loads are done once only those behind them are outstanding; the slot before has been read
+            wait_vmcnt_dyn(ops - mark[0]);
+            asm volatile("" ::: "memory");
+            issue(filled + ((slot + kStreamSlots - 1) & (kStreamSlots - 1)) * kStreamStage);
+            mark[0] = mark[1];
+            mark[1] = mark[2];
+            mark[2] = ops;
+            const char *st = ring + slot * kStreamStage;
+            frag af[2][4], bf[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (ASTRIDED) af[s][i] = read_strided<128>(st + aofs[i] + s * (32 * 128));
+                    else af[s][i] = *(const frag *)(st + (alo ^ (s * 64)) + i * 2048);
+                }
+                bf[s] = *(const frag *)(st + (blo ^ (s * 64)));
+            }
+            wait_lgkm0();
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i][0] = P::mma(af[s][i], bf[s], acc[i][0]);
+            slot = (slot + 1) & (kStreamSlots - 1);
+        }
+        cta_barrier();                                // the previous tile's sums have been read
+        if (wid > 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) parts[((wid - 1) * 4 + i) * 64 + lane] = __builtin_bit_cast(u32x4, acc[i][0]);
+        }
+        wait_lgkm0();
+        cta_barrier();
+        if (wid > 0) continue;
+#pragma unroll
+        for (int w = 0; w < 3; ++w)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i][0] += __builtin_bit_cast(typename P::acc, parts[(w * 4 + i) * 64 + lane]);
+        int e, ft, row0, valid;
+        list.find(t, lane, e, ft, row0, valid);
+        product_store<DT, 4, 1, false>(a, acc, e, ft * 64, row0, valid, 0, lane);
+    }
+}
+
 template <void (*KERNEL)(ProductPass)>
-hipError_t product_launch(unsigned grid, int lds, const ProductPass &p, hipStream_t s) {
+hipError_t product_launch(unsigned grid, int threads, int lds, const ProductPass &p, hipStream_t s) {
     static std::atomic<uint64_t> allowed{0};
     const hipError_t e = allow_lds((const void *)KERNEL, lds, allowed);
     if (e != hipSuccess) return e;
-    KERNEL<<<grid, kProductThreads, lds, s>>>(p);
+    KERNEL<<<grid, threads, lds, s>>>(p);
     return hipGetLastError();
 }
 
 // ---- rounding to 8-bit integers ----------------------------------------------
 
-// A row's largest magnitude, then its codes; a wave takes a row.
-template <int DT>
+// A row's largest magnitude, then its codes.  WAVES waves take a row, eight values a lane at a time; up to four times eight stay in registers between the two, longer rows are read again.  A row of 7168 by one wave
+// takes 47 us however few there are, by four 4.6; short rows keep more lanes at work with a wave each.
+constexpr int kInt8Held = 4;
+
+template <int DT, int WAVES>
 __global__ __launch_bounds__(256) void int8_quantize_kernel(const void *__restrict__ x, int64_t ld, int64_t rows, int cols,
                                                             int run, int8_t *__restrict__ q, float *__restrict__ s) {
-    const int lane = threadIdx.x & 63;
-    for (int64_t r = blockIdx.x * 4ll + (threadIdx.x >> 6); r < rows; r += gridDim.x * 4ll) {
-        auto at = [&](int c) {
-            return DT == DT_F32 ? ((const float *)x)[r * ld + c] : bf16_to_f32(((const uint16_t *)x)[r * ld + c]);
+    constexpr int ROWS = 4 / WAVES, LANES = WAVES * 64;
+    __shared__ float tops[4];
+    const int in = threadIdx.x % LANES, wave = threadIdx.x >> 6;
+    for (int64_t r0 = blockIdx.x * (int64_t)ROWS; r0 < rows; r0 += gridDim.x * (int64_t)ROWS) {
+        const int64_t r = r0 + threadIdx.x / LANES;
+        const bool there = r < rows;
+        float held[kInt8Held][8];
+        // the largest magnitude as bits: those of an infinity or NaN are larger than any number's
+        uint32_t top = __float_as_uint(0x1p-100f);
+        auto look = [&](const float (&v)[8]) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
         };
-        float top = 0.0f;
-        bool bad = false;
-        for (int c = lane; c < cols; c += 64) {
-            const float v = fabsf(at(c));
-            bad |= !(v <= 3.4028235e38f);
-            top = fmaxf(top, v);
+#pragma unroll
+        for (int i = 0; i < kInt8Held; ++i) {
+            const int c = (i * LANES + in) * 8;
+            load8<DT>(x, r * ld + c, there ? min(8, cols - c) : 0, held[i]);
+            look(held[i]);
         }
-        bad = __ballot(bad) != 0;
-        top = fmaxf(wave_max_f32(top), 0x1p-100f);
-        const float inv = bad ? 0.0f : 127.0f / top;
-        for (int c = lane; c < run; c += 64)
-            q[r * run + c] = c < cols && !bad ? (int8_t)(int)rintf(at(c) * inv) : (int8_t)0;
-        if (lane == 0) s[r] = bad ? __uint_as_float(0x7FC00000u) : top / 127.0f;
+        for (int c = (kInt8Held * LANES + in) * 8; there && c < cols; c += LANES * 8) {
+            float v[8];
+            load8<DT>(x, r * ld + c, cols - c, v);
+            look(v);
+        }
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m, kWave));
+        if (WAVES > 1) {
+            __syncthreads();                        // the row before has been read
+            tops[wave] = __uint_as_float(top);
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) top = max(top, __float_as_uint(tops[w]));
+        }
+        if (!there) continue;
+        const bool bad = top >= 0x7F800000u;
+        const float most = __uint_as_float(top), inv = 127.0f / most;
+        auto codes = [&](const float (&v)[8], int c) {
+            uint32_t w[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k >> 2] |= ((uint32_t)(int)rintf(v[k] * inv) & 0xFFu) << (8 * (k & 3));
+            if (c < run) *(u32x2 *)(q + r * run + c) = bad ? u32x2{0, 0} : u32x2{w[0], w[1]};
+        };
+#pragma unroll
+        for (int i = 0; i < kInt8Held; ++i) codes(held[i], (i * LANES + in) * 8);
+        for (int c = (kInt8Held * LANES + in) * 8; c < run; c += LANES * 8) {
+            float v[8];
+            load8<DT>(x, r * ld + c, cols - c, v);
+            codes(v, c);
+        }
+        if (in == 0) s[r] = bad ? __uint_as_float(0x7FC00000u) : most / 127.0f;
     }
 }
 
 }  // namespace
 
 hipError_t launch_product(int dt, int op, const ProductPass &p, hipStream_t s) {
-    const unsigned grid = (unsigned)((device_cus() + 7) / 8 * 8);
+    using std::integral_constant;
+    const int64_t cus = device_cus();
+    const unsigned grid = (unsigned)((cus + 7) / 8 * 8);
     const int esz = dt == DT_I8 ? 1 : 2;
     auto aligned = [&](const void *ptr, int64_t ld) { return (uintptr_t)ptr % 16 == 0 && ld * esz % 16 == 0; };
-    // loads of whole 16-byte pieces; a piece has to lie in its row
-    const bool direct = aligned(p.a, p.a_ld) && aligned(p.b, p.b_ld) && p.a_mat * esz % 16 == 0 &&
+    // loads of whole 16-byte pieces: a piece has to lie in its row
+    const bool pieces = aligned(p.a, p.a_ld) && aligned(p.b, p.b_ld) && p.a_mat * esz % 16 == 0 &&
                         (op == PRODUCT_DW ? p.A % 8 == 0 && p.B % 8 == 0
                                           : (int64_t)p.K * esz % 16 == 0 && (op == PRODUCT_Y || p.A % 8 == 0));
-    const bool many = p.max_rows > 160ll * p.n_exp;
     if (op == PRODUCT_DW) {
-        if (direct) return product_launch<product_kernel<DT_BF16, PRODUCT_DW, 8, true>>(grid, product_lds<8>(), p, s);
-        return product_launch<product_kernel<DT_BF16, PRODUCT_DW, 8, false>>(grid, product_lds<8>(), p, s);
+        if (pieces && p.wide) return product_launch<product_dw_kernel>(grid, kProductThreads, kDwLds, p, s);
+        return product_launch<product_kernel<DT_BF16, PRODUCT_DW, 8, false>>(grid, kProductThreads, product_lds<8>(), p, s);
     }
-    if (op == PRODUCT_DX) {
-        if (!direct) return product_launch<product_kernel<DT_BF16, PRODUCT_DX, 4, false>>(grid, product_lds<4>(), p, s);
-        if (many) return product_launch<product_kernel<DT_BF16, PRODUCT_DX, 8, true>>(grid, product_lds<8>(), p, s);
-        return product_launch<product_kernel<DT_BF16, PRODUCT_DX, 4, true>>(grid, product_lds<4>(), p, s);
-    }
-    if (dt == DT_I8) {
-        if (many) return product_launch<product_kernel<DT_I8, PRODUCT_Y, 8, true>>(grid, product_lds<8>(), p, s);
-        return product_launch<product_kernel<DT_I8, PRODUCT_Y, 4, true>>(grid, product_lds<4>(), p, s);
-    }
-    if (!direct) return product_launch<product_kernel<DT_BF16, PRODUCT_Y, 4, false>>(grid, product_lds<4>(), p, s);
-    if (many) return product_launch<product_kernel<DT_BF16, PRODUCT_Y, 8, true>>(grid, product_lds<8>(), p, s);
-    return product_launch<product_kernel<DT_BF16, PRODUCT_Y, 4, true>>(grid, product_lds<4>(), p, s);
+    auto of = [&](auto dtc, auto opc) {
+        constexpr int D = decltype(dtc)::value, O = decltype(opc)::value;
+        switch (product_variant(p.max_rows, p.n_exp, p.A, pieces, cus)) {
+            case kProductStream:
+                return product_launch<product_stream_kernel<D, O == PRODUCT_DX>>(grid, kStreamThreads, kStreamLds, p, s);
+            case kProduct160:
+                return product_launch<product_kernel<D, O, 5, true>>(grid, kProductThreads, product_lds<5>(), p, s);
+            case kProduct256:
+                return product_launch<product_kernel<D, O, 8, true>>(grid, kProductThreads, product_lds<8>(), p, s);
+            default:
+                // codes of 8 bits always lie in pieces
+                if constexpr (D == DT_I8) return hipErrorInvalidValue;
+                else return product_launch<product_kernel<D, O, 4, false>>(grid, kProductThreads, product_lds<4>(), p, s);
+        }
+    };
+    if (dt == DT_I8) return of(integral_constant<int, DT_I8>{}, integral_constant<int, PRODUCT_Y>{});
+    if (op == PRODUCT_DX) return of(integral_constant<int, DT_BF16>{}, integral_constant<int, PRODUCT_DX>{});
+    return of(integral_constant<int, DT_BF16>{}, integral_constant<int, PRODUCT_Y>{});
 }
 
 hipError_t launch_int8_quantize(int dt, const void *x, int64_t ld, int64_t rows, int cols, int8_t *q, float *sc,
                                 hipStream_t s) {
     if (rows <= 0) return hipSuccess;
     const int run = (int)int8_row(cols);
-    const unsigned grid = (unsigned)(rows < 65536 ? (rows + 3) / 4 : 16384);
-    if (dt == DT_F32) int8_quantize_kernel<DT_F32><<<grid, 256, 0, s>>>(x, ld, rows, cols, run, q, sc);
-    else int8_quantize_kernel<DT_BF16><<<grid, 256, 0, s>>>(x, ld, rows, cols, run, q, sc);
-    return hipGetLastError();
+    auto launch = [&](auto dtc, auto waves) {
+        constexpr int D = decltype(dtc)::value, W = decltype(waves)::value;
+        const int64_t groups = (rows * W + 3) / 4;
+        int8_quantize_kernel<D, W><<<(unsigned)(groups < 65536 ? groups : 65536), 256, 0, s>>>(x, ld, rows, cols, run, q, sc);
+        return hipGetLastError();
+    };
+    using std::integral_constant;
+    auto of = [&](auto dtc) {
+        return cols <= 512 * kInt8Held ? launch(dtc, integral_constant<int, 1>{}) : launch(dtc, integral_constant<int, 4>{});
+    };
+    return dt == DT_F32 ? of(integral_constant<int, DT_F32>{}) : of(integral_constant<int, DT_BF16>{});
 }
 
 }  // namespace moe

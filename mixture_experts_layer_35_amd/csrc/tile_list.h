@@ -61,5 +61,12 @@ struct TileList {
     }
 };
 
+// A value of a kernel's read-only arrays at an address that all lanes share, by a scalar load: it does not wait behind the
+// vector loads under way.
+__device__ __forceinline__ int scalar_load(const int32_t *p, int64_t i) {
+    typedef const __attribute__((address_space(4))) int32_t constant_int;
+    return ((constant_int *)(uintptr_t)p)[i];
+}
+
 }  // namespace
 }  // namespace moe

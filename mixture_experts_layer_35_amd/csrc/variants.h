@@ -61,6 +61,29 @@ inline Mx4Variant mx4_variant(int64_t max_rows, int64_t n_exp, int64_t kruns, in
     return fewer && blocks(kMx4Tile160) * ((ftiles + 3) / 4) >= cus ? kMx4Tile160 : kMx4Tile128;
 }
 
+// ---- products of experts -------------------------------------------------------
+enum ProductVariant {
+    kProductAny,        // operands through registers: rows that do not lie at multiples of 16 bytes
+    kProductStream,     // tiles of 64 features by up to 8 rows, four waves a tile
+    kProduct160,        // tiles of 256 features by up to 160 rows, three stages of LDS
+    kProduct256,        // by up to 256 rows, two stages
+};
+
+// Rows of a tile.
+constexpr int product_rows(ProductVariant v) { return v == kProductStream ? 8 : v == kProduct160 ? 160 : v == kProduct256 ? 256 : 128; }
+
+// features: the output's (the inputs of the gradient at x); pieces: whether operands lie in pieces of 16 bytes.
+inline ProductVariant product_variant(int64_t max_rows, int64_t n_exp, int64_t features, bool pieces, int64_t cus) {
+    if (!pieces) return kProductAny;
+    const int64_t experts = max_rows < n_exp ? max_rows : n_exp;
+    // small tiles as long as there are no more than two for each compute unit
+    const int64_t small = (experts + (max_rows - experts) / product_rows(kProductStream)) * ((features + 63) / 64);
+    if (small <= 2 * cus) return kProductStream;
+    // 32 experts, 512 rows: 7168 to 2048 577 us in tiles of 256 rows.  256 experts, 128 rows: 1560 us in tiles of 160 with a stage
+    // more, 1686 with 128, which half of the experts need two of
+    return max_rows > 160 * n_exp ? kProduct256 : kProduct160;
+}
+
 // ---- orthogonalised updates ----------------------------------------------------
 enum OrthVariant { kOrth256x256, kOrth256x128, kOrth128x128 };   // a tile's sides along a and b
 
