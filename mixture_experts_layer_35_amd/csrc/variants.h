@@ -87,18 +87,24 @@ inline ProductVariant product_variant(int64_t max_rows, int64_t n_exp, int64_t f
 // ---- orthogonalised updates ----------------------------------------------------
 enum OrthVariant { kOrth256x256, kOrth256x128, kOrth128x128 };   // a tile's sides along a and b
 
-// The tiles that end soonest: rounds of tiles over the workgroups, each as long as its products.
+// The tiles that end soonest: rounds of tiles over the workgroups, each as long as one tile takes.  A tile of 256 x 256 takes
+// 2.2 to 3.1 times as long as one of 128 x 128, one of 256 x 128 1.4 to 1.7 times.  Microseconds with 256 x 256, 256 x 128 and
+// 128 x 128: 8 matrices of 2048 x 7168, X X^T 907, 818, 887, P X 1178, 1349, 1621; one of them 381, 236, 169 and 150, 178,
+// 225; 32 of 512 x 1024, X X^T 70, 45, 57.
 inline OrthVariant orth_variant(int64_t n, int64_t A, int64_t B, bool symmetric, int64_t workgroups) {
-    auto time = [&](int64_t ta, int64_t tb) {
+    auto time = [&](int64_t ta, int64_t tb, int64_t tile) {
         const int64_t at = (A + ta - 1) / ta, bt = (B + tb - 1) / tb;
-        int64_t tiles = 0;
-        for (int64_t i = 0; i < at; ++i) {
-            const int64_t above = symmetric ? i * ta / tb : 0;
-            tiles += bt - (above < bt ? above : bt);
+        int64_t tiles = at * bt;
+        if (symmetric) {
+            tiles = 0;
+            for (int64_t i = 0; i < at; ++i) {
+                const int64_t above = i * ta / tb;
+                tiles += bt - (above < bt ? above : bt);
+            }
         }
-        return (n * tiles + workgroups - 1) / workgroups * ta * tb;
+        return (n * tiles + workgroups - 1) / workgroups * tile;
     };
-    const int64_t big = time(256, 256), mid = time(256, 128), small = time(128, 128);
+    const int64_t big = time(256, 256, 26), mid = time(256, 128, 16), small = time(128, 128, 10);
     if (big <= mid && big <= small) return kOrth256x256;
     return mid <= small ? kOrth256x128 : kOrth128x128;
 }

@@ -15,8 +15,10 @@ import torch
 
 from . import (MOE_BF16, MOE_E4M3, MOE_F32, MOE_WS_FORWARD, MOE_WS_PERMUTE, MoeShape, make_gate_rule, make_shape,
                moe_backward, moe_backward_workspace_bytes, moe_combine, moe_dequantize_mx4, moe_ffn_mx4_workspace_bytes,
-               moe_forward, moe_gate, moe_gate_backward, moe_grouped_ffn_mx4, moe_permute, moe_quantize_mx4,
-               moe_quantize_weights_128x128, moe_transpose_expert_weights, moe_workspace_bytes)
+               moe_forward, moe_gate, moe_gate_backward, moe_grouped_ffn_mx4, moe_grouped_product, moe_grouped_product_dw,
+               moe_grouped_product_dx, moe_grouped_product_int8, moe_orthogonalize, moe_orthogonalize_workspace_bytes,
+               moe_permute, moe_quantize_int8, moe_quantize_mx4, moe_quantize_weights_128x128, moe_transpose_expert_weights,
+               moe_workspace_bytes)
 from . import _stream as _raw
 
 
@@ -113,6 +115,141 @@ def dequantize_mx4(q: torch.Tensor, s: torch.Tensor, cols: int, dtype=torch.bflo
         y = torch.empty(q.shape[:-1] + (cols,), dtype=dtype, device=q.device)
     moe_dequantize_mx4(y.numel() // cols, cols, q, s, _float_type(y), y, cols, stream)
     return y
+
+
+# ---- products of experts ------------------------------------------------------------------------
+
+
+@contextlib.contextmanager
+def _at(stream, device):
+    """`device` and `stream` (its current one if None) are the current ones inside."""
+    with torch.cuda.device(device), torch.cuda.stream(_torch_stream(stream, device)):
+        yield
+
+
+def _batch(offsets, gather, n, rows, device):
+    """Checks the experts' bounds and the rows' tokens; the number of rows."""
+    _check("offsets", offsets, device, (torch.int32,), (n + 1,))
+    if gather is None:
+        return rows
+    _check("gather", gather, device, (torch.int32,), (gather.numel(),))
+    return gather.numel()
+
+
+def _out(name, out, shape, dtype, device):
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("%s: bf16 or fp32 expected, not %s" % (name, dtype))
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(name, out, device, (dtype,), shape, dense=False)
+    return out
+
+
+def grouped_product(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, gather: torch.Tensor = None,
+                    dtype=torch.bfloat16, out: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """y[r] = w[e] x[gather[r]] for the rows offsets[e] <= r < offsets[e + 1] of expert e.
+
+    x [tokens][in] bf16 (rows may be padded), w [n][out][in] bf16, offsets [n + 1] and gather [rows] int32 (None: a row for
+    each token), all on one GPU; y [rows][out] bf16 or fp32.  Rows from offsets[n] on are left as they were."""
+    _on_gpu(x, w, offsets)
+    n, cout, cin = w.shape
+    _check("x", x, w.device, (torch.bfloat16,), (x.shape[0], cin), dense=False)
+    _check("w", w, w.device, (torch.bfloat16,), w.shape)
+    rows = _batch(offsets, gather, n, x.shape[0], w.device)
+    with _at(stream, w.device):
+        y = _out("out", out, (rows, cout), dtype, w.device)
+        moe_grouped_product(n, offsets, rows, gather, cin, cout, x, _row_stride(x), w, _float_type(y), y, _row_stride(y))
+    return y
+
+
+def grouped_product_dx(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, dtype=torch.bfloat16,
+                       out: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """The gradient of grouped_product at the rows of x: dx[r] = w[e]^T dy[r], [rows][in], from dy [rows][out] bf16.  A token's
+    gradient is the sum of its rows'."""
+    _on_gpu(dy, w, offsets)
+    n, cout, cin = w.shape
+    _check("dy", dy, w.device, (torch.bfloat16,), (dy.shape[0], cout), dense=False)
+    _check("w", w, w.device, (torch.bfloat16,), w.shape)
+    rows = _batch(offsets, None, n, dy.shape[0], w.device)
+    with _at(stream, w.device):
+        dx = _out("out", out, (rows, cin), dtype, w.device)
+        moe_grouped_product_dx(n, offsets, rows, cin, cout, dy, _row_stride(dy), w, _float_type(dx), dx, _row_stride(dx))
+    return dx
+
+
+def grouped_product_dw(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tensor, gather: torch.Tensor = None,
+                       dtype=torch.float32, add_to: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """The gradient of grouped_product at w: dw[e] = the sum over the expert's rows of dy[r] x[gather[r]]^T, [n][out][in].
+    add_to: an fp32 gradient that the sums are added to, in place."""
+    _on_gpu(x, dy, offsets)
+    n, cin, cout = offsets.numel() - 1, x.shape[1], dy.shape[1]
+    _check("x", x, x.device, (torch.bfloat16,), (x.shape[0], cin), dense=False)
+    rows = _batch(offsets, gather, n, x.shape[0], x.device)
+    _check("dy", dy, x.device, (torch.bfloat16,), (rows, cout), dense=False)
+    with _at(stream, x.device):
+        if add_to is not None:
+            _check("add_to", add_to, x.device, (torch.float32,), (n, cout, cin))
+        dw = _out("dw", add_to, (n, cout, cin), torch.float32 if add_to is not None else dtype, x.device)
+        moe_grouped_product_dw(n, offsets, rows, gather, cin, cout, x, _row_stride(x), dy, _row_stride(dy), _float_type(dw),
+                               dw, add_to is not None)
+    return dw
+
+
+def quantize_int8(x: torch.Tensor, stream=None):
+    """bf16/fp32 device tensor [..., cols] whose rows are contiguous and evenly spaced -> (codes [..., 128 R] int8 with zeros
+    behind the last value, scales [...] fp32), R = ceil(cols / 128): a scale a token, or for weights one an output channel."""
+    _on_gpu(x)
+    cols = x.shape[-1]
+    rows = x.view(-1, cols) if x.numel() else x.reshape(0, cols)
+    with _at(stream, x.device):
+        q = torch.empty(x.shape[:-1] + (-(-cols // 128) * 128,), dtype=torch.int8, device=x.device)
+        s = torch.empty(x.shape[:-1], device=x.device)
+        moe_quantize_int8(rows.shape[0], cols, _float_type(x), rows, _row_stride(rows), q, s)
+    return q, s
+
+
+def grouped_product_int8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, cols: int,
+                         offsets: torch.Tensor, gather: torch.Tensor = None, dtype=torch.bfloat16,
+                         out: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """grouped_product of quantize_int8's tokens x [tokens][128 R], x_scales [tokens] and weights w [n][out][128 R], w_scales
+    [n][out], of `cols` values a row."""
+    _on_gpu(x, x_scales, w, w_scales, offsets)
+    n, cout = w_scales.shape
+    run = -(-cols // 128) * 128
+    _check("x", x, w.device, (torch.int8,), (x.shape[0], run))
+    _check("x_scales", x_scales, w.device, (torch.float32,), (x.shape[0],))
+    _check("w", w, w.device, (torch.int8,), (n, cout, run))
+    _check("w_scales", w_scales, w.device, (torch.float32,), (n, cout))
+    rows = _batch(offsets, gather, n, x.shape[0], w.device)
+    with _at(stream, w.device):
+        y = _out("out", out, (rows, cout), dtype, w.device)
+        moe_grouped_product_int8(n, offsets, rows, gather, cols, cout, x, x_scales, w, w_scales, _float_type(y), y,
+                                 _row_stride(y))
+    return y
+
+
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=None, eps: float = 1e-7, scale: float = 1.0,
+                  out: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """scale times the matrices g [..., rows, cols] (bf16 or fp32, contiguous) brought near their nearest orthogonal ones by
+    Newton-Schulz steps, bf16.  coefficients: (a, b, c) for all steps or a list of them (default NEWTON_SCHULZ)."""
+    _on_gpu(g)
+    _check("g", g, g.device, (torch.bfloat16, torch.float32), g.shape)
+    rows, cols = g.shape[-2:]
+    n = g.numel() // max(1, rows * cols)
+    c = [tuple(v) for v in coefficients] if coefficients is not None and not isinstance(coefficients[0], (int, float)) \
+        else [tuple(coefficients or NEWTON_SCHULZ)] * steps
+    if len(c) != steps or any(len(v) != 3 for v in c):
+        raise ValueError("three coefficients for each of %d steps expected" % steps)
+    with _at(stream, g.device):
+        if out is None:
+            out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+        _check("out", out, g.device, (torch.bfloat16,), g.shape)
+        ws = torch.empty(moe_orthogonalize_workspace_bytes(n, rows, cols) if n else 0, dtype=torch.uint8, device=g.device)
+        moe_orthogonalize(n, rows, cols, _float_type(g), g, steps, [x for v in c for x in v], eps, scale, out, ws)
+    return out
 
 
 class MoeLayer:

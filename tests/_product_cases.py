@@ -5,7 +5,7 @@ import torch
 SHAPES = [
     ([1], 8, 8), ([3], 1, 1), ([0, 1, 0], 7, 5), ([1, 1, 1, 1], 64, 16), ([5, 0, 2, 17], 72, 40), ([33, 1, 0, 64], 136, 264),
     ([130, 2, 31], 200, 304), ([16] * 9, 1000, 360), ([0, 0, 0], 64, 64), ([257, 300, 0, 511], 320, 520),
-    ([161, 1, 90], 513, 257), ([700], 192, 136), ([4] * 70, 128, 72), ([40, 65, 100, 129, 170, 200, 231, 256], 96, 280),
+    ([161, 1, 90], 513, 257), ([700], 192, 136), ([4] * 70, 128, 72), ([40, 65, 100, 129, 170, 200, 231, 256], 96, 280), ([300] * 9, 1536, 1600), ([161, 1, 40] * 20, 256, 1544),
 ]
 # x_ld - in, first element's place, y_ld - out, first element's place
 LAYOUTS = [(0, 0, 0, 0), (8, 8, 8, 8), (3, 1, 5, 1)]

@@ -80,10 +80,14 @@ def test_random_matrices(moe, n, rows, cols, dtype):
         check(y[i], *exact(g[i]))
 
 
+# each pair of tile sides in each product
+MORE = [(8, 700, 1300), (2, 900, 1000), (64, 512, 256), (3, 1536, 160), (16, 768, 800), (32, 512, 600), (70, 256, 256), (130, 130, 260), (200, 200, 230)]
+
+
 def test_sizes_take_every_kernel(moe):
-    """Many and few, large and small matrices: each pair of tile sides in each product."""
+    """Many and few, large and small matrices."""
     gen = torch.Generator().manual_seed(4)
-    for n, rows, cols in ((8, 700, 1300), (2, 900, 1000), (64, 512, 256), (3, 1536, 160), (16, 768, 800)):
+    for n, rows, cols in MORE:
         g = torch.randn((n, rows, cols), generator=gen)
         y = run(moe, g.cuda())
         for i in (0, n - 1):

@@ -1,0 +1,165 @@
+"""Refusals of the grouped products, the 8-bit products and the orthogonalised updates, before any HIP call; and which kernel a
+call takes by csrc/variants.h, asked without a GPU: the GPU tests' sizes reach every variant."""
+import os
+import subprocess
+
+import pytest
+
+import mixture_experts_layer_35_amd as moe
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 1 << 20     # an aligned non-null address; rejected calls never dereference it
+BAD, UNSUP, WS, OK = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED, moe.MOE_ERR_WORKSPACE, moe.MOE_OK
+BF16, F32, E4M3 = moe.MOE_BF16, moe.MOE_F32, moe.MOE_E4M3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(moe.LIB_PATH):
+        from mixture_experts_layer_35_amd import build
+        build.build()
+    return moe.lib()
+
+
+def product(lib, n=4, offsets=FAKE, rows=10, gather=None, cin=64, out=32, x=FAKE, x_ld=None, w=FAKE, dt=BF16, y=FAKE, y_ld=None):
+    return lib.moe_grouped_product(n, offsets, rows, gather, cin, out, x, cin if x_ld is None else x_ld, w, dt, y,
+                                   out if y_ld is None else y_ld, None)
+
+
+def dx(lib, n=4, offsets=FAKE, rows=10, gather=None, cin=64, out=32, x=FAKE, x_ld=None, w=FAKE, dt=BF16, y=FAKE, y_ld=None):
+    return lib.moe_grouped_product_dx(n, offsets, rows, cin, out, x, out if x_ld is None else x_ld, w, dt, y,
+                                      cin if y_ld is None else y_ld, None)
+
+
+def dw(lib, n=4, offsets=FAKE, rows=10, gather=None, cin=64, out=32, x=FAKE, x_ld=None, w=FAKE, dt=F32, y=FAKE, y_ld=None, acc=0):
+    return lib.moe_grouped_product_dw(n, offsets, rows, gather, cin, out, x, cin if x_ld is None else x_ld, y,
+                                      out if y_ld is None else y_ld, dt, w, acc, None)
+
+
+def int8(lib, n=4, offsets=FAKE, rows=10, gather=None, cin=64, out=32, x=FAKE, x_ld=None, w=FAKE, dt=BF16, y=FAKE, y_ld=None, xs=FAKE,
+         ws=FAKE):
+    return lib.moe_grouped_product_int8(n, offsets, rows, gather, cin, out, x, xs, w, ws, dt, y, out if y_ld is None else y_ld,
+                                        None)
+
+
+CALLS = [product, dx, dw, int8]
+
+
+@pytest.mark.parametrize("call", CALLS, ids=lambda f: f.__name__)
+def test_sizes(lib, call):
+    for change in (dict(n=0), dict(n=-1), dict(rows=-1), dict(cin=0), dict(out=-2), dict(y_ld=7)):
+        assert call(lib, **change) == BAD, change
+    for change in (dict(n=1025), dict(rows=1 << 31), dict(cin=(1 << 20) + 1, out=1), dict(cin=1 << 15, out=(1 << 14) + 1),
+                   dict(dt=E4M3), dict(rows=(1 << 31) - 1, cin=4096, out=4096)):
+        assert call(lib, **change) == UNSUP, change
+        assert "moe_grouped_product" in moe.moe_last_error()
+    if call is not int8:
+        assert call(lib, x_ld=31) == BAD
+
+
+@pytest.mark.parametrize("call", CALLS, ids=lambda f: f.__name__)
+def test_pointers(lib, call):
+    for name in ("offsets", "x", "w", "y") + (("xs", "ws") if call is int8 else ()):
+        assert call(lib, **{name: None}) == BAD and "must not be NULL" in moe.moe_last_error()
+    for name in ("x", "w", "y"):
+        assert call(lib, **{name: FAKE + 1}) == BAD and "aligned" in moe.moe_last_error()
+    if call is not dw:
+        assert call(lib, rows=0, offsets=None, x=None, w=None, y=None) == OK
+
+
+def test_what_only_one_of_them_refuses(lib):
+    assert dw(lib, dt=BF16, acc=1) == UNSUP
+    assert dw(lib, dt=F32, w=FAKE + 2) == BAD and product(lib, dt=F32, y=FAKE + 2) == BAD
+    assert int8(lib, cin=131073, out=1) == UNSUP
+    assert int8(lib, x=FAKE + 8) == BAD and int8(lib, w=FAKE + 8) == BAD
+    assert int8(lib, xs=FAKE + 2) == BAD and int8(lib, ws=FAKE + 2) == BAD
+
+
+def test_rounding(lib):
+    q = lib.moe_quantize_int8
+    assert q(-1, 8, F32, FAKE, 8, FAKE, FAKE, None) == BAD and q(1, 0, F32, FAKE, 8, FAKE, FAKE, None) == BAD
+    assert q(1, 8, F32, FAKE, 7, FAKE, FAKE, None) == BAD and q(1, 8, E4M3, FAKE, 8, FAKE, FAKE, None) == UNSUP
+    assert q(1, (1 << 30) + 1, BF16, FAKE, 1 << 31, FAKE, FAKE, None) == UNSUP
+    for x, c, s in ((None, FAKE, FAKE), (FAKE, None, FAKE), (FAKE, FAKE, None), (FAKE + 2, FAKE, FAKE), (FAKE, FAKE + 8, FAKE),
+                    (FAKE, FAKE, FAKE + 1)):
+        assert q(1, 8, F32, x, 8, c, s, None) == BAD
+    assert q(0, 8, F32, None, 8, None, None, None) == OK
+
+
+def orth(lib, n=2, rows=40, cols=50, dt=F32, g=FAKE, steps=1, coeffs=None, eps=1e-7, y=FAKE, ws=FAKE, ws_bytes=1 << 30):
+    import ctypes
+    c = (ctypes.c_float * 3)(1.5, -0.5, 0.0)
+    return lib.moe_orthogonalize(n, rows, cols, dt, g, steps, ctypes.cast(c, ctypes.c_void_p) if coeffs is None else None, eps, 1.0, y, ws,
+                                 ws_bytes, None)
+
+
+def test_orthogonalize(lib):
+    for change in (dict(n=-1), dict(rows=0), dict(cols=-3), dict(steps=0), dict(steps=65), dict(eps=-1.0), dict(eps=float("nan")),
+                   dict(coeffs=False), dict(g=None), dict(y=None), dict(g=FAKE + 2), dict(y=FAKE + 1), dict(ws=FAKE + 128)):
+        assert orth(lib, **change) == BAD, change
+    for change in (dict(dt=E4M3), dict(n=65536), dict(rows=16385, cols=16385), dict(rows=16384, cols=16385), dict(rows=1, cols=1 << 24),
+                   dict(n=4097, rows=16384, cols=16384)):
+        assert orth(lib, **change) == UNSUP, change
+    assert orth(lib, ws=None) == WS and orth(lib, ws_bytes=100) == WS
+    assert orth(lib, n=0, g=None, y=None, ws=None) == OK
+    need = lib.moe_orthogonalize_workspace_bytes
+    for n, r, c in ((1, 1, 1), (2, 40, 50), (8, 2048, 7168), (24, 1000, 360), (64, 7168, 24)):
+        a, b = (-(-v // 32) * 32 for v in sorted((r, c)))
+        assert 8 * n * a * (a + b) <= need(n, r, c) <= 8 * n * a * (a + b) + 512 * n + 1024
+    assert need(1, 0, 1) == 0 and need(-1, 1, 1) == 0
+    with pytest.raises(ValueError):
+        moe.moe_orthogonalize(1, 2, 2, F32, FAKE, 2, (1.0, 2.0, 3.0), 0.0, 1.0, FAKE, None)
+    with pytest.raises(moe.MoeError):
+        moe.moe_orthogonalize_workspace_bytes(1, 1 << 20, 1 << 20)
+
+
+SOURCE = """
+#include <cstdio>
+#include "variants.h"
+int main() {
+    char what;
+    long long a, b, c, d;
+    while (std::scanf(" %c %lld %lld %lld %lld", &what, &a, &b, &c, &d) == 5)
+        std::printf("%d\\n", what == 'p' ? (int)moe::product_variant(a, b, c, d != 0, 256) : (int)moe::orth_variant(a, b, c, d != 0, 256));
+    return 0;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def ask(tmp_path_factory):
+    d = tmp_path_factory.mktemp("variants")
+    (d / "ask.cpp").write_text(SOURCE)
+    csrc = os.path.join(ROOT, "mixture_experts_layer_35_amd", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", csrc, str(d / "ask.cpp"), "-o", str(d / "ask")], check=True)
+
+    def lines(queries):
+        text = "".join("%s %d %d %d %d\n" % q for q in queries)
+        out = subprocess.run([str(d / "ask")], input=text, capture_output=True, text=True, check=True).stdout.split()
+        assert len(out) == len(queries)
+        return [int(v) for v in out]
+
+    return lines
+
+
+def test_gpu_tests_reach_every_product_kernel(ask):
+    pytest.importorskip("torch")
+    from _product_cases import SHAPES
+    y = [("p", sum(c) + 3, len(c), out, cin % 8 == 0) for c, cin, out in SHAPES]
+    gradient = [("p", sum(c) + 3, len(c), cin, cin % 8 == 0 and out % 8 == 0) for c, cin, out in SHAPES]
+    codes = [("p", sum(c) + 2, len(c), out, 1) for c, cin, out in SHAPES]
+    assert set(ask(y)) == set(ask(gradient)) == {0, 1, 2, 3}
+    assert set(ask(codes)) == {1, 2, 3}
+    # one token, a decode batch and a prompt of 256 experts; 512 rows each
+    assert ask([("p", r, n, 2048, 1) for r, n in ((8, 256), (1024, 256), (32768, 256), (16384, 32))]) == [1, 2, 2, 3]
+
+
+def test_gpu_tests_reach_every_orthogonalize_kernel(ask):
+    pytest.importorskip("torch")
+    from test_gpu_orthogonalize import SIZES, MORE
+    got = {True: set(), False: set()}
+    for n, rows, cols in SIZES + MORE:
+        a, b = (-(-v // 32) * 32 for v in sorted((rows, cols)))
+        got[True] |= set(ask([("o", n, a, a, 1)]))
+        got[False] |= set(ask([("o", n, b, a, 0)]))
+    assert got[True] == got[False] == {0, 1, 2}
