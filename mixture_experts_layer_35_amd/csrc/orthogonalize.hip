@@ -137,22 +137,23 @@ struct OrthPass {
     int r, cc, tall;            // sides of X without padding
 };
 
-// A tile is 64 RB values of a against 32 CAP of b; eight waves, 4 along a by 2 along b (16-row blocks of b in turn).
-template <int RB, int CAP>
+// Eight waves, WA along a by 8 / WA along b (16-row blocks of b in turn), each with RB blocks of 16 values of a and CB of b.
+template <int RB, int CB, int WA>
 struct OrthTile {
-    static constexpr int TA = RB * 64, TB = CAP * 32;
+    static constexpr int WB = 8 / WA, TA = RB * 16 * WA, TB = CB * 16 * WB;
     static constexpr int stage_a = TA * 128, stage = stage_a + TB * 128;
     static constexpr int scratch = 8 * 16 * 17 * 4;     // a 16 x 16 block of each wave, turned over
-    static constexpr int slots = (160 * 1024 - scratch) / stage < 4 ? (160 * 1024 - scratch) / stage : 4;
+    static constexpr int slots = (160 * 1024 - scratch) / stage < 8 ? (160 * 1024 - scratch) / stage : 8;
     static constexpr int lds = slots * stage + scratch;
 };
 
-template <int OP, int RB, int CAP>
+template <int OP, int RB, int CAP, int WA>
 __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a) {
-    typedef OrthTile<RB, CAP> T;
+    typedef OrthTile<RB, CAP, WA> T;
     constexpr bool SYM = OP != ORTH_UPDATE, ASTRIDED = OP == ORTH_UPDATE;
-    constexpr int SLOTS = T::slots, STAGE = T::stage, QB = CAP / 2, N = RB + QB;
-    static_assert(CAP % 2 == 0 && SLOTS >= 2, "loads of a step are shared evenly");
+    constexpr int SLOTS = T::slots, STAGE = T::stage, WB = T::WB, QA = T::TA / 64, QB = T::TB / 64, N = QA + QB;
+    constexpr int ROW = T::TA * 4, LANES = ROW / 16;   // a staged row of the reduction: bytes, lanes that bring it
+    static_assert(T::TA % 64 == 0 && T::TB % 64 == 0 && RB % 2 == 0 && SLOTS >= 2, "loads of a step are shared evenly");
     extern __shared__ __align__(1024) char smem[];
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     char *const ring = smem;
@@ -190,7 +191,7 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
     // ---- loads ----
     int it = first, ik = 0;
     i32x4s ar, br;
-    uint32_t avoff[RB], bvoff[QB];
+    uint32_t avoff[QA], bvoff[QB];
     const int a_step = ASTRIDED ? 32 * a.A * 4 : 128;
     auto bytes_at = [&](int row) { return ((lane & 7) ^ swz<128>(row)) << 4; };
     auto aim = [&]() __attribute__((always_inline)) {
@@ -200,15 +201,13 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
         ar = words_of(a.a + m * amat, amat * 2);
         br = words_of(a.b + m * bmat, bmat * 2);
 #pragma unroll
-        for (int q = 0; q < RB; ++q) {
+        for (int q = 0; q < QA; ++q) {
             if (ASTRIDED) {
-                // 16 bytes number (lane, or its low half) of row k of the step
-                const int k = RB == 4 ? wid * 4 + q : wid * 4 + q * 2 + (lane >> 5);
-                const int piece = (RB == 4 ? lane : lane & 31) ^ strided_slot(k);
-                const int col = a0 * 4 + piece * 16;
+                const int k = (wid * QA + q) * (64 / LANES) + lane / LANES;
+                const int col = a0 * 4 + (((lane % LANES) ^ strided_slot(k)) << 4);
                 avoff[q] = col < a.A * 4 ? (uint32_t)(k * a.A * 4 + col) : kNoOffset;
             } else {
-                const int row = wid * (RB * 8) + q * 8 + (lane >> 3);
+                const int row = (wid * QA + q) * 8 + (lane >> 3);
                 avoff[q] = a0 + row < a.A ? (uint32_t)((a0 + row) * a.K * 4 + bytes_at(row)) : kNoOffset;
             }
         }
@@ -222,9 +221,9 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
     auto issue = [&](int slot) __attribute__((always_inline)) {
         if (it >= end) return 0;
         if (ik == 0) aim();
-        const int as = filled + slot * STAGE + wid * (RB * 1024), bs = filled + slot * STAGE + T::stage_a + wid * 1024;
+        const int as = filled + slot * STAGE + wid * (QA * 1024), bs = filled + slot * STAGE + T::stage_a + wid * 1024;
 #pragma unroll
-        for (int q = 0; q < RB; ++q) fill16(ar, avoff[q], ik * a_step, as + q * 1024);
+        for (int q = 0; q < QA; ++q) fill16(ar, avoff[q], ik * a_step, as + q * 1024);
 #pragma unroll
         for (int q = 0; q < QB; ++q) fill16(br, bvoff[q], ik * 128, bs + q * 8192);
         if (++ik == steps) {
@@ -235,7 +234,7 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
     };
 
     // ---- products ----
-    const int wf = wid >> 1, wm = wid & 1, r15 = lane & 15, g = lane >> 4;
+    const int wf = wid / WB, wm = wid % WB, r15 = lane & 15, g = lane >> 4;
     const int arow = wf * (RB * 16) + r15, brow = wm * 16 + r15;
     const int alo = arow * 128 + ((g ^ swz<128>(arow)) << 4), blo = brow * 128 + ((g ^ swz<128>(brow)) << 4);
     int aofs[RB][2];
@@ -247,7 +246,7 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
             for (int p = 0; p < 2; ++p) {
                 const int col = wf * (RB * 16) + i * 16 + 4 * aa;
                 const int piece = ((col >> 5) * 128 + p * 64 + (col & 31) * 2) >> 4;
-                aofs[i][p] = k * (RB * 256) + ((piece ^ strided_slot(k)) << 4) + 8 * (aa & 1);
+                aofs[i][p] = k * ROW + ((piece ^ strided_slot(k)) << 4) + 8 * (aa & 1);
             }
     }
     int slot = 0;
@@ -274,8 +273,8 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 if constexpr (ASTRIDED) {
-                    ah[i] = read_strided<RB * 256>(as + aofs[i][0]);
-                    al[i] = read_strided<RB * 256>(as + aofs[i][1]);
+                    ah[i] = read_strided<ROW>(as + aofs[i][0]);
+                    al[i] = read_strided<ROW>(as + aofs[i][1]);
                 } else {
                     ah[i] = *(const bf16x8 *)(as + alo + i * 2048);
                     al[i] = *(const bf16x8 *)(as + (alo ^ 64) + i * 2048);
@@ -283,7 +282,7 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
             }
 #pragma unroll
             for (int j = 0; j < CAP; ++j) {
-                const bf16x8 bh = *(const bf16x8 *)(bs + blo + j * 4096), bl = *(const bf16x8 *)(bs + (blo ^ 64) + j * 4096);
+                const bf16x8 bh = *(const bf16x8 *)(bs + blo + j * (WB * 2048)), bl = *(const bf16x8 *)(bs + (blo ^ 64) + j * (WB * 2048));
 #pragma unroll
                 for (int i = 0; i < RB; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ah[i], bh, acc[i][j], 0, 0, 0);
 #pragma unroll
@@ -300,7 +299,7 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
         const int64_t ld = (int64_t)a.A * 2, mat = (int64_t)m * a.B * ld;
 #pragma unroll
         for (int j = 0; j < CAP; ++j) {
-            const int bb = b0 + (j * 2 + wm) * 16, b = bb + r15;
+            const int bb = b0 + (j * WB + wm) * 16, b = bb + r15;
 #pragma unroll
             for (int i = 0; i < RB; i += 2) {
                 const int f0 = a0 + wf * (RB * 16) + i * 16;           // a run of 32 values of a
@@ -383,9 +382,10 @@ template <int OP>
 hipError_t orth_product(const OrthPass &p, hipStream_t s) {
     const unsigned grid = (unsigned)((device_cus() + 7) / 8 * 8);
     switch (orth_variant(p.n, p.A, p.B, OP != ORTH_UPDATE, grid)) {
-        case kOrth256x256: return orth_launch<orth_kernel<OP, 4, 8>>(grid, OrthTile<4, 8>::lds, p, s);
-        case kOrth256x128: return orth_launch<orth_kernel<OP, 4, 4>>(grid, OrthTile<4, 4>::lds, p, s);
-        default: return orth_launch<orth_kernel<OP, 2, 4>>(grid, OrthTile<2, 4>::lds, p, s);
+        case kOrth256x256: return orth_launch<orth_kernel<OP, 4, 8, 4>>(grid, OrthTile<4, 8, 4>::lds, p, s);
+        case kOrth256x128: return orth_launch<orth_kernel<OP, 4, 4, 4>>(grid, OrthTile<4, 4, 4>::lds, p, s);
+        case kOrth128x128: return orth_launch<orth_kernel<OP, 2, 4, 4>>(grid, OrthTile<2, 4, 4>::lds, p, s);
+        default: return orth_launch<orth_kernel<OP, 2, 1, 2>>(grid, OrthTile<2, 1, 2>::lds, p, s);
     }
 }
 

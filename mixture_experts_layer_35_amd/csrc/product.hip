@@ -56,13 +56,29 @@ struct Product<DT_I8> {
 // 16 bytes that lanes without data read.
 __device__ const u32x4 product_zeros = {0, 0, 0, 0};
 
-// Values e0 .. e0 + 7 of a bf16 row of `n` values at any address, zeros past its end.
-__device__ __forceinline__ u32x4 row_chunk(const uint16_t *row, int64_t e0, int64_t n) {
-    if (e0 + 8 <= n) return *(const u32x4_any *)(row + e0);
-    u32x4 v = {0, 0, 0, 0};
+// Values e0 .. e0 + 7 of a bf16 row of `n` values at any address, zeros past its end.  The load of a piece that ends past the row
+// is moved back to the row's last eight values, which are then shifted: no lane branches around its load.
+__device__ __forceinline__ u32x4 row_chunk(const uint16_t *row, int e0, int n) {
+    if (n < 8) {
+        u32x4 v = {0, 0, 0, 0};
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (e0 + k < n) v[k >> 1] |= (uint32_t)row[e0 + k] << (16 * (k & 1));
+        for (int k = 0; k < 8; ++k)
+            if (e0 + k < n) v[k >> 1] |= (uint32_t)row[e0 + k] << (16 * (k & 1));
+        return v;
+    }
+    const int e = min(e0, n - 8), d = min(e0 - e, 8);
+    u32x4 v = *(const u32x4_any *)(row + e);
+    if (d > 0) {
+        uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+        if (d >= 4) {
+            lo = d == 8 ? 0 : hi >> (16 * (d - 4));
+            hi = 0;
+        } else {
+            lo = lo >> (16 * d) | hi << (64 - 16 * d);
+            hi >>= 16 * d;
+        }
+        v = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+    }
     return v;
 }
 
@@ -93,38 +109,36 @@ __device__ __forceinline__ void product_store(const ProductPass &a, const Acc (&
                 }
             }
         const int64_t at = (DW ? ((int64_t)e * a.B + row0 + b) : (int64_t)row0 + b) * a.out_ld;
+        // 16-byte stores at any address (the memory pipeline takes them); single values where a row ends within one
         if (a.out_f32) {
             float *row = (float *)a.out + at;
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 const int f = f0 + i * 16 + 4 * g;
                 if (!there) continue;
-                if (a.wide && f < a.A) {
+                if (f + 4 <= a.A) {
                     f32x4 o = {v[i][0], v[i][1], v[i][2], v[i][3]};
-                    if (a.accumulate) o += *(const f32x4 *)(row + f);
-                    *(f32x4 *)(row + f) = o;
-                } else if (!a.wide) {
+                    if (DW && a.accumulate) o += *(const f32x4_any *)(row + f);
+                    *(f32x4_any *)(row + f) = o;
+                } else {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (f + q < a.A) row[f + q] = v[i][q] + (a.accumulate ? row[f + q] : 0.0f);
+                    for (int q = 0; q < 3; ++q)
+                        if (f + q < a.A) row[f + q] = v[i][q] + (DW && a.accumulate ? row[f + q] : 0.0f);
                 }
             }
         } else {
             uint16_t *row = (uint16_t *)a.out + at;
 #pragma unroll
             for (int i = 0; i < RB; i += 2) {
-                if (a.wide) {
-                    const u32x4 o = pair_bf16_value(v[i], v[i + 1], lane);
-                    const int f = pair_bf16_col(f0 + i * 16, lane);
-                    if (there && f < a.A) *(u32x4 *)(row + f) = o;
-                } else if (there) {
+                const u32x4 o = pair_bf16_value(v[i], v[i + 1], lane);
+                const int f = pair_bf16_col(f0 + i * 16, lane);
+                if (!there) continue;
+                if (f + 8 <= a.A) {
+                    *(u32x4_any *)(row + f) = o;
+                } else {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int f = f0 + (i + h) * 16 + 4 * g + q;
-                            if (f < a.A) row[f] = (uint16_t)pack_bf16x2(v[i + h][q], 0.0f);
-                        }
+                    for (int q = 0; q < 7; ++q)
+                        if (f + q < a.A) row[f + q] = (uint16_t)(o[q >> 1] >> (16 * (q & 1)));
                 }
             }
         }
@@ -134,8 +148,9 @@ __device__ __forceinline__ void product_store(const ProductPass &a, const Acc (&
 template <int DT, int OP, int CAP, bool DIRECT>
 __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const ProductPass a) {
     typedef Product<DT> P;
-    constexpr int esz = P::esz, SLOTS = DIRECT ? product_slots<CAP>() : 2, STAGE = product_stage<CAP>();
+    constexpr int esz = P::esz, SLOTS = DIRECT ? product_slots<CAP>() : 2;
     constexpr bool DW = OP == PRODUCT_DW, ASTRIDED = OP != PRODUCT_Y;
+    constexpr int STAGE = DW ? 2 * kProductStageA : product_stage<CAP>();
     static_assert(!DW || !DIRECT, "product_dw_kernel");
     constexpr int QB = CAP / 2 + CAP % 2;            // loads of B a wave issues for a step, at most
     extern __shared__ __align__(1024) char smem[];
@@ -146,7 +161,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
     for (int i = tid; i < a.n_exp; i += kProductThreads)
         ends[i] = (int)max((int64_t)0, min((int64_t)a.offsets[i + 1], a.max_rows));
     __syncthreads();
-    const int atiles = (a.A + kTileA - 1) / kTileA, btiles = DW ? (a.B + 255) / 256 : 0;
+    const int atiles = (a.A + kTileA - 1) / kTileA, btiles = DW ? (a.B + CAP * 32 - 1) / (CAP * 32) : 0;
     TileList list;
     int total;
     if (DW) {
@@ -168,8 +183,8 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
             e = t / (atiles * btiles);
             const int rest = t - e * (atiles * btiles), bt = rest / atiles;
             a0 = (rest - bt * atiles) * kTileA;
-            row0 = bt * 256;
-            valid = min(256, a.B - row0);
+            row0 = bt * (CAP * 32);
+            valid = min(CAP * 32, a.B - row0);
         } else {
             int ft;
             list.find(t, lane, e, ft, row0, valid);
@@ -180,7 +195,10 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
     auto first_of = [&](int e) { return __builtin_amdgcn_readfirstlane(list.start(e)); };
     auto rows_of = [&](int e) { return __builtin_amdgcn_readfirstlane(ends[e]) - first_of(e); };
     constexpr int KSTEP = 128 / esz;                  // of the reduction
-    auto steps_of = [&](int e) __attribute__((always_inline)) { return DW ? max(1, (rows_of(e) + KSTEP - 1) / KSTEP) : (a.K + KSTEP - 1) / KSTEP; };
+    auto steps_of = [&](int e) __attribute__((always_inline)) {
+        const int n = DW ? max(1, (rows_of(e) + KSTEP - 1) / KSTEP) : (a.K + KSTEP - 1) / KSTEP;
+        return DIRECT ? n : (n + 1) & ~1;             // through registers in twos, the last one of zeros
+    };
 
     // ---- loads: the tile and step that come next ----
     int it = first, ik = 0, isteps = 0, ie = 0, ia0 = 0, irow0 = 0, ivalid = 0;
@@ -225,17 +243,6 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
             }
         }
     };
-    // A strided operand's 16 bytes of load q in step k (dw): row r of the reduction, values c .. c + 7
-    auto dw_chunk = [&](int q, bool isA, const uint16_t *&row, int &c) __attribute__((always_inline)) {
-        const int k = ak0 + q * 2, r = ik * 64 + k, m = rows_of(ie);
-        const int64_t R = first_of(ie) + min(r, max(m - 1, 0));
-        c = (isA ? ia0 : irow0) + values_at(k);
-        row = nullptr;
-        if (r < m && c < (isA ? a.A : a.B)) {
-            const int64_t src = isA && a.gather ? (int64_t)a.gather[R] : R;
-            row = isA ? (const uint16_t *)a.a + src * a.a_ld : (const uint16_t *)a.b + src * a.b_ld;
-        }
-    };
     const int64_t kbytes = (int64_t)a.K * esz;
     // issues a step's loads into a stage; the number of loads
     auto issue = [&](int stage) __attribute__((always_inline)) {
@@ -273,45 +280,57 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
         }
         return n;
     };
-    // the same through registers, for rows that do not lie at multiples of 16 bytes
-    u32x4 areg[4], breg[DW ? 4 : QB];
-    int iblocks = 0;
-    auto fetch = [&]() __attribute__((always_inline)) {
-        iblocks = 0;
+    // the same through registers, for rows that do not lie at multiples of 16 bytes: two sets, so that a step's loads have two steps'
+    // time (4 rows to 4 experts of 6581 x 1793, the gradient at x: 79 us, with one set 141)
+    u32x4 areg[2][4], breg[2][DW ? 4 : QB];
+    int iblocks[2] = {0, 0};
+    auto fetch = [&](auto setc) __attribute__((always_inline)) {
+        constexpr int S = decltype(setc)::value;
+        iblocks[S] = 0;
         if (it >= end) return;
         if (ik == 0) aim();
+        constexpr u32x4 none = {0, 0, 0, 0};
         if constexpr (DW) {
+            const int m = rows_of(ie), lo = first_of(ie);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const uint16_t *row;
-                int c;
-                dw_chunk(q, true, row, c);
-                areg[q] = row ? row_chunk(row, c, a.A) : u32x4{0, 0, 0, 0};
-                dw_chunk(q, false, row, c);
-                breg[q] = row ? row_chunk(row, c, a.B) : u32x4{0, 0, 0, 0};
+                areg[S][q] = breg[S][q] = none;
+                if (ik * 64 + wid * 8 + q * 2 < m) {             // the load's first row, the same in all lanes
+                    const int k = ak0 + q * 2, r = ik * 64 + k;
+                    const int64_t R = lo + min(r, m - 1), src = a.gather ? (int64_t)a.gather[R] : R;
+                    const u32x4 x = row_chunk((const uint16_t *)a.a + src * a.a_ld, ia0 + values_at(k), a.A);
+                    const u32x4 y = row_chunk((const uint16_t *)a.b + R * a.b_ld, irow0 + values_at(k) % (CAP * 32), a.B);
+                    areg[S][q] = r < m ? x : none;
+                    breg[S][q] = r < m ? y : none;
+                }
             }
-            iblocks = 8;
+            iblocks[S] = 8;
         } else {
             const uint16_t *m = (const uint16_t *)a.a + (int64_t)ie * a.a_mat;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 if (!ASTRIDED) {
                     const int row = arow0 + q * 8;
-                    areg[q] = ia0 + row < a.A ? row_chunk(m + (int64_t)(ia0 + row) * a.a_ld,
-                                                          (int64_t)ik * 64 + bytes_at(row) / 2, a.K)
-                                              : u32x4{0, 0, 0, 0};
+                    areg[S][q] = none;
+                    if (ia0 + wid * 32 + q * 8 < a.A) {          // the load's first row, the same in all lanes
+                        const u32x4 v = row_chunk(m + (int64_t)min(ia0 + row, a.A - 1) * a.a_ld, ik * 64 + bytes_at(row) / 2, a.K);
+                        areg[S][q] = ia0 + row < a.A ? v : none;
+                    }
                 } else {
-                    const int k = ak0 + q * 2;
-                    areg[q] = ik * 64 + k < a.K ? row_chunk(m + (int64_t)(ik * 64 + k) * a.a_ld, ia0 + values_at(k), a.A)
-                                                : u32x4{0, 0, 0, 0};
+                    const int k = ik * 64 + ak0 + q * 2;
+                    areg[S][q] = none;
+                    if (ik * 64 + wid * 8 + q * 2 < a.K) {
+                        const u32x4 v = row_chunk(m + (int64_t)min(k, a.K - 1) * a.a_ld, ia0 + values_at(ak0 + q * 2), a.A);
+                        areg[S][q] = k < a.K ? v : none;
+                    }
                 }
             }
-            iblocks = (ivalid + 31) >> 5;
+            iblocks[S] = (ivalid + 31) >> 5;
 #pragma unroll
             for (int q = 0; q < QB; ++q)
-                if (q * 8 + wid < iblocks * 4) {
+                if (q * 8 + wid < iblocks[S] * 4) {
                     const int at = bytes_at((q * 8 + wid) * 8 + (lane >> 3)) / 2;
-                    breg[q] = row_chunk((const uint16_t *)bptr[q] - at, (int64_t)ik * 64 + at, a.K);
+                    breg[S][q] = row_chunk((const uint16_t *)bptr[q] - at, ik * 64 + at, a.K);
                 }
         }
         if (++ik == isteps) {
@@ -319,18 +338,19 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
             it += step;
         }
     };
-    auto put = [&](char *stage) __attribute__((always_inline)) {
-        if (!iblocks) return;
+    auto put = [&](auto setc, char *stage) __attribute__((always_inline)) {
+        constexpr int S = decltype(setc)::value;
+        if (!iblocks[S]) return;
         char *as = stage + wid * 4096 + lane * 16, *bs = stage + kProductStageA + lane * 16;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) *(u32x4 *)(as + q * 1024) = areg[q];
+        for (int q = 0; q < 4; ++q) *(u32x4 *)(as + q * 1024) = areg[S][q];
         if constexpr (DW) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) *(u32x4 *)(bs + wid * 4096 + q * 1024) = breg[q];
+            for (int q = 0; q < 4; ++q) *(u32x4 *)(bs + wid * 4096 + q * 1024) = breg[S][q];
         } else {
 #pragma unroll
             for (int q = 0; q < QB; ++q)
-                if (q * 8 + wid < iblocks * 4) *(u32x4 *)(bs + (q * 8 + wid) * 1024) = breg[q];
+                if (q * 8 + wid < iblocks[S] * 4) *(u32x4 *)(bs + (q * 8 + wid) * 1024) = breg[S][q];
         }
     };
 
@@ -354,17 +374,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
     auto tile = [&](auto tbc, int steps, int e, int a0, int row0, int valid) __attribute__((always_inline)) {
         constexpr int TB = decltype(tbc)::value;
         typename P::acc acc[4][TB] = {};
-        for (int k = 0; k < steps; ++k) {
-            // the stage's loads are done once only the later stages' are outstanding; past the barrier every wave's are, and
-            // the stage before has been read
-            if (DIRECT) {
-                if (SLOTS == 3) wait_vmcnt_dyn(n1);
-                else wait_vmcnt<0>();
-            }
-            wait_lgkm0();
-            cta_barrier();
-            if (DIRECT) n1 = issue(filled + (SLOTS == 3 ? next(next(slot)) : next(slot)) * STAGE);
-            else fetch();
+        auto products = [&]() __attribute__((always_inline)) {
             const char *as = ring + slot * STAGE, *bs = as + kProductStageA;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -385,8 +395,36 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[i][j] = P::mma(af[i], bf[j], acc[i][j]);
             }
-            if (!DIRECT) put(ring + next(slot) * STAGE);
-            slot = next(slot);
+        };
+        if constexpr (DIRECT) {
+            for (int k = 0; k < steps; ++k) {
+                // the stage's loads are done once only the later stages' are outstanding; past the barrier every wave's are,
+                // and the stage before has been read
+                if (SLOTS == 3) wait_vmcnt_dyn(n1);
+                else wait_vmcnt<0>();
+                wait_lgkm0();
+                cta_barrier();
+                n1 = issue(filled + (SLOTS == 3 ? next(next(slot)) : next(slot)) * STAGE);
+                products();
+                slot = next(slot);
+            }
+        } else {
+            using std::integral_constant;
+            // past the barrier the slot is filled and the other one has been read; set p of registers goes to slot p
+            for (int k = 0; k < steps; k += 2) {
+                wait_lgkm0();
+                cta_barrier();
+                fetch(integral_constant<int, 0>{});
+                products();
+                put(integral_constant<int, 1>{}, ring + STAGE);
+                slot = 1;
+                wait_lgkm0();
+                cta_barrier();
+                fetch(integral_constant<int, 1>{});
+                products();
+                put(integral_constant<int, 0>{}, ring);
+                slot = 0;
+            }
         }
         product_store<DT, 4, TB, DW>(a, acc, e, a0 + wf * 64, row0, valid, wm, lane);
     };
@@ -394,8 +432,9 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
         issue(filled);
         if (SLOTS == 3) n1 = issue(filled + STAGE);
     } else {
-        fetch();
-        put(ring);
+        fetch(std::integral_constant<int, 0>{});
+        put(std::integral_constant<int, 0>{}, ring);
+        fetch(std::integral_constant<int, 1>{});
     }
     for (int t = first; t < end; t += step) {
         int e, a0, row0, valid;
@@ -798,6 +837,8 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(const void *__restri
 
 }  // namespace
 
+constexpr int kDwAnyLds = kEndBytes + 2 * 2 * kProductStageA;   // both operands' stages hold 256 values a row
+
 hipError_t launch_product(int dt, int op, const ProductPass &p, hipStream_t s) {
     using std::integral_constant;
     const int64_t cus = device_cus();
@@ -810,7 +851,7 @@ hipError_t launch_product(int dt, int op, const ProductPass &p, hipStream_t s) {
                                           : (int64_t)p.K * esz % 16 == 0 && (op == PRODUCT_Y || p.A % 8 == 0));
     if (op == PRODUCT_DW) {
         if (pieces && p.wide) return product_launch<product_dw_kernel>(grid, kProductThreads, kDwLds, p, s);
-        return product_launch<product_kernel<DT_BF16, PRODUCT_DW, 8, false>>(grid, kProductThreads, product_lds<8>(), p, s);
+        return product_launch<product_kernel<DT_BF16, PRODUCT_DW, 4, false>>(grid, kProductThreads, kDwAnyLds, p, s);
     }
     auto of = [&](auto dtc, auto opc) {
         constexpr int D = decltype(dtc)::value, O = decltype(opc)::value;

@@ -85,7 +85,7 @@ inline ProductVariant product_variant(int64_t max_rows, int64_t n_exp, int64_t f
 }
 
 // ---- orthogonalised updates ----------------------------------------------------
-enum OrthVariant { kOrth256x256, kOrth256x128, kOrth128x128 };   // a tile's sides along a and b
+enum OrthVariant { kOrth256x256, kOrth256x128, kOrth128x128, kOrth64x64 };   // a tile's sides along a and b
 
 // The tiles that end soonest: rounds of tiles over the workgroups, each as long as one tile takes.  A tile of 256 x 256 takes
 // 2.2 to 3.1 times as long as one of 128 x 128, one of 256 x 128 1.4 to 1.7 times.  Microseconds with 256 x 256, 256 x 128 and
@@ -105,8 +105,10 @@ inline OrthVariant orth_variant(int64_t n, int64_t A, int64_t B, bool symmetric,
         return (n * tiles + workgroups - 1) / workgroups * tile;
     };
     const int64_t big = time(256, 256, 26), mid = time(256, 128, 16), small = time(128, 128, 10);
-    if (big <= mid && big <= small) return kOrth256x256;
-    return mid <= small ? kOrth256x128 : kOrth128x128;
+    const int64_t least = time(64, 64, 4);
+    if (big <= mid && big <= small && big <= least) return kOrth256x256;
+    if (mid <= small && mid <= least) return kOrth256x128;
+    return small <= least ? kOrth128x128 : kOrth64x64;
 }
 
 }  // namespace moe
