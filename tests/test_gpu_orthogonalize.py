@@ -81,7 +81,8 @@ def test_random_matrices(moe, n, rows, cols, dtype):
 
 
 # each pair of tile sides in each product
-MORE = [(8, 700, 1300), (2, 900, 1000), (64, 512, 256), (3, 1536, 160), (16, 768, 800), (32, 512, 600), (70, 256, 256), (130, 130, 260), (200, 200, 230)]
+MORE = [(8, 700, 1300), (2, 900, 1000), (64, 512, 256), (3, 1536, 160), (16, 768, 800), (32, 512, 600), (70, 256, 256), (130, 130, 260), (200, 200, 230), (20, 90, 800), (20, 160, 790), (40, 780, 160),
+        (60, 220, 224), (60, 285, 288), (60, 400, 410)]
 
 
 def test_sizes_take_every_kernel(moe):

@@ -162,4 +162,4 @@ def test_gpu_tests_reach_every_orthogonalize_kernel(ask):
         a, b = (-(-v // 32) * 32 for v in sorted((rows, cols)))
         got[True] |= set(ask([("o", n, a, a, 1)]))
         got[False] |= set(ask([("o", n, b, a, 0)]))
-    assert got[True] == got[False] == {0, 1, 2}
+    assert got[True] == got[False] == {0, 1, 2, 3}
