@@ -38,8 +38,8 @@
  *   - Matrices of weights are stored [out][in] (the reduction dimension is
  *     contiguous).  bf16 is stored as its 16-bit pattern; e4m3 is OCP E4M3FN
  *     (largest finite 448) in one byte.
- *   - Inputs must be finite; NaN and infinity are not checked (the gate and MX4
- *     calls say what they make of them).
+ *   - Inputs must be finite; NaN and infinity are not checked (the gate, MX4,
+ *     product and update calls say what they make of them).
  *   - Calls on different streams that share a buffer race, workspaces
  *     included (a workspace holds intermediate results and the expert
  *     kernel's tile-queue counters); the library holds no global mutable

@@ -1361,7 +1361,6 @@ int moe_grouped_product(int32_t n_exp, const int32_t *offsets, int64_t max_rows,
     p.out = y;
     p.out_ld = y_ld;
     p.out_f32 = y_dtype == MOE_F32;
-    p.wide = wide_rows(y, y_ld, out, y_dtype);
     HIPCHK(launch_product(DT_BF16, PRODUCT_Y, p, (hipStream_t)stream));
     return MOE_OK;
 }
@@ -1396,7 +1395,6 @@ int moe_grouped_product_dx(int32_t n_exp, const int32_t *offsets, int64_t max_ro
     p.out = dx;
     p.out_ld = dx_ld;
     p.out_f32 = dx_dtype == MOE_F32;
-    p.wide = wide_rows(dx, dx_ld, in, dx_dtype);
     HIPCHK(launch_product(DT_BF16, PRODUCT_DX, p, (hipStream_t)stream));
     return MOE_OK;
 }
@@ -1493,7 +1491,6 @@ int moe_grouped_product_int8(int32_t n_exp, const int32_t *offsets, int64_t max_
     p.out = y;
     p.out_ld = y_ld;
     p.out_f32 = y_dtype == MOE_F32;
-    p.wide = wide_rows(y, y_ld, out, y_dtype);
     p.sa = w_scales;
     p.sb = x_scales;
     HIPCHK(launch_product(DT_I8, PRODUCT_Y, p, (hipStream_t)stream));

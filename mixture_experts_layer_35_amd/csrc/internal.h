@@ -80,7 +80,7 @@ struct ProductPass {
     void *out;
     int64_t out_ld;
     int out_f32, accumulate;
-    int wide;               // rows of out take 16-byte stores
+    int wide;               // PRODUCT_DW: rows of out lie at multiples of 16 bytes
     const float *sa, *sb;   // DT_I8: scales of the features [n_exp][A] and of the tokens
 };
 // dt: DT_BF16, or DT_I8 for PRODUCT_Y.

@@ -247,7 +247,9 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=None, eps: float
         if out is None:
             out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
         _check("out", out, g.device, (torch.bfloat16,), g.shape)
-        ws = torch.empty(moe_orthogonalize_workspace_bytes(n, rows, cols) if n else 0, dtype=torch.uint8, device=g.device)
+        if n == 0:
+            return out
+        ws = torch.empty(moe_orthogonalize_workspace_bytes(n, rows, cols), dtype=torch.uint8, device=g.device)
         moe_orthogonalize(n, rows, cols, _float_type(g), g, steps, [x for v in c for x in v], eps, scale, out, ws)
     return out
 

@@ -169,6 +169,39 @@ def test_infinities_and_nan_stay_where_they_belong(moe, cin, cout):
         assert (got[inf] == want[inf]).all() and fine.any() and not fine.all()
 
 
+@pytest.mark.parametrize("cin,cout", [(7168, 64), (7161, 63)], ids=["pieces", "odd"])
+def test_rows_past_32_bits(moe, cin, cout):
+    """Tokens that lie more than 4 GiB behind the first one, few rows of an expert and many."""
+    tokens = (1 << 32) // (2 * cin) + 400
+    x = torch.empty((tokens, cin), dtype=BF16, device="cuda")
+    counts = [3, 300]
+    rows = sum(counts)
+    offsets, _, g = ref.batch(counts, 6)
+    far = ref.integers(g, rows, cin)
+    x[tokens - rows:] = far.to(BF16).cuda()
+    order = torch.randperm(rows, generator=g)
+    gather = (tokens - rows + order).to(torch.int32)
+    w, dy = ref.integers(g, 2, cout, cin), ref.integers(g, rows, cout)
+    o, gd, wd, dd = offsets.cuda(), gather.cuda(), w.to(BF16).cuda(), dy.to(BF16).cuda()
+    y = torch.empty((rows, cout), device="cuda")
+    moe.moe_grouped_product(2, o, rows, gd, cin, cout, x, cin, wd, moe.MOE_F32, y, cout)
+    assert (y.double().cpu() == ref.product(counts, far, order, w)).all()
+    few = torch.tensor([0, 3, 3], dtype=torch.int32, device="cuda")
+    y.zero_()
+    moe.moe_grouped_product(2, few, 3, gd, cin, cout, x, cin, wd, moe.MOE_F32, y, cout)
+    assert (y[:3].double().cpu() == ref.product([3], far, order[:3], w)).all() and (y[3:] == 0).all()
+    dw = torch.empty((2, cout, cin), device="cuda")
+    moe.moe_grouped_product_dw(2, o, rows, gd, cin, cout, x, cin, dd, cout, moe.MOE_F32, dw, False)
+    assert (dw.double().cpu() == ref.product_dw(counts, far, order, dy)).all()
+    # results that far apart: rows of y in a wide buffer
+    ld = (1 << 32) // (4 * (rows - 4))
+    wide = torch.empty(ld * rows, device="cuda")
+    v = wide.view(rows, ld)[:, :cout]
+    moe.moe_grouped_product(2, o, rows, gd, cin, cout, x, cin, wd, moe.MOE_F32, v, ld)
+    moe.moe_grouped_product(2, o, rows, gd, cin, cout, x, cin, wd, moe.MOE_F32, y, cout)
+    assert (v == y).all()
+
+
 # ---- 8-bit integers -----------------------------------------------------------------------------
 
 
