@@ -196,7 +196,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
     auto rows_of = [&](int e) { return __builtin_amdgcn_readfirstlane(ends[e]) - first_of(e); };
     constexpr int KSTEP = 128 / esz;                  // of the reduction
     auto steps_of = [&](int e) __attribute__((always_inline)) {
-        const int n = DW ? max(1, (rows_of(e) + KSTEP - 1) / KSTEP) : (a.K + KSTEP - 1) / KSTEP;
+        const int n = DW ? max(1, parts_of(rows_of(e), KSTEP)) : (a.K + KSTEP - 1) / KSTEP;
         return DIRECT ? n : (n + 1) & ~1;             // through registers in twos, the last one of zeros
     };
 
@@ -492,7 +492,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_dw_kernel(const Pr
     auto start_of = [&](int e) { return e ? __builtin_amdgcn_readfirstlane(ends[e - 1]) : 0; };
     auto rows_of = [&](int e) { return max(0, __builtin_amdgcn_readfirstlane(ends[e]) - start_of(e)); };
     // an expert without rows takes one step of zeros
-    auto steps_of = [&](int rows) { return max(1, (rows + 31) / 32); };
+    auto steps_of = [&](int rows) { return max(1, parts_of(rows, 32)); };
 
     // ---- loads: the tile and step that come next, and the rows of x that this wave's loads of it bring ----
     const int k0 = wid * 4 + (lane >> 5);             // the lane's row of a step, in load 0; load 1 is two on
@@ -528,7 +528,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_dw_kernel(const Pr
             const bool there = r < rows;
             const int64_t xrow = lane >> 5 ? index[q * 2 + 1] : index[q * 2];
             const char *x = (const char *)a.a + xrow * a.a_ld * 2 + aoff[q];
-            const char *y = (const char *)a.b + (int64_t)(lo + r) * a.b_ld * 2 + boff[q];
+            const char *y = (const char *)a.b + ((int64_t)lo + r) * a.b_ld * 2 + boff[q];
             fill16(there && aoff[q] >= 0 ? x : (const char *)&product_zeros, stage + wid * 2048 + q * 1024);
             fill16(there && boff[q] >= 0 ? y : (const char *)&product_zeros, stage + kDwStage / 2 + wid * 2048 + q * 1024);
         }

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "parts.h"
+
 namespace moe {
 namespace {
 
@@ -32,7 +34,7 @@ struct TileList {
         total = __builtin_amdgcn_readlane(run, 63);
     }
     __device__ int start(int e) const { return e ? ends[e - 1] : 0; }
-    __device__ int blocks(int e) const { return (ends[e] - start(e) + bm - 1) / bm; }
+    __device__ int blocks(int e) const { return parts_of(ends[e] - start(e), bm); }
     // Tile t < total (the same in all lanes): expert, feature tile, first row and number of rows.  An expert's
     // token blocks of `unit` rows are split evenly over its row blocks, so that at most one is part empty.
     __device__ void find(int t, int lane, int &e, int &ft, int &row0, int &valid) const {
@@ -50,10 +52,10 @@ struct TileList {
         rest = __builtin_amdgcn_readlane(rest, owner);
         const int first = __builtin_amdgcn_readfirstlane(start(e));
         const int m = __builtin_amdgcn_readfirstlane(ends[e]) - first;
-        const int mt = (m + bm - 1) / bm;
+        const int mt = parts_of(m, bm);
         // quotients are vector instructions: back to scalars, which the descriptors have to be
         ft = __builtin_amdgcn_readfirstlane(rest / mt);
-        const int unit = min(bm, 32), units = (m + unit - 1) / unit;
+        const int unit = min(bm, 32), units = parts_of(m, unit);
         const int block = rest - ft * mt, uq = __builtin_amdgcn_readfirstlane(units / mt), ur = units - uq * mt;
         const int r = (block * uq + min(block, ur)) * unit;
         row0 = first + r;
