@@ -200,6 +200,9 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
         return DIRECT ? n : (n + 1) & ~1;             // through registers in twos, the last one of zeros
     };
 
+    // added to: an expert without rows keeps its values to the bit, so its tiles are passed over by loads and products alike
+    auto kept = [&](int t) { return DW && a.accumulate && rows_of(t / (atiles * btiles)) <= 0; };
+
     // ---- loads: the tile and step that come next ----
     int it = first, ik = 0, isteps = 0, ie = 0, ia0 = 0, irow0 = 0, ivalid = 0;
     i32x4s ar;
@@ -287,6 +290,8 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
     auto fetch = [&](auto setc) __attribute__((always_inline)) {
         constexpr int S = decltype(setc)::value;
         iblocks[S] = 0;
+        if (DW && ik == 0)
+            while (it < end && kept(it)) it += step;
         if (it >= end) return;
         if (ik == 0) aim();
         constexpr u32x4 none = {0, 0, 0, 0};
@@ -437,6 +442,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
         fetch(std::integral_constant<int, 1>{});
     }
     for (int t = first; t < end; t += step) {
+        if (kept(t)) continue;
         int e, a0, row0, valid;
         find(t, e, a0, row0, valid);
         const int steps = steps_of(e);
@@ -491,7 +497,11 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_dw_kernel(const Pr
     };
     auto start_of = [&](int e) { return e ? __builtin_amdgcn_readfirstlane(ends[e - 1]) : 0; };
     auto rows_of = [&](int e) { return max(0, __builtin_amdgcn_readfirstlane(ends[e]) - start_of(e)); };
-    // an expert without rows takes one step of zeros
+    // an expert without rows takes one step of zeros, or none: added to, it keeps its values to the bit, so its tiles are passed
+    // over by loads and products alike
+    auto kept = [&](int t) {
+        return a.accumulate && rows_of(__builtin_amdgcn_readfirstlane(t / (atiles * btiles))) == 0;
+    };
     auto steps_of = [&](int rows) { return max(1, parts_of(rows, 32)); };
 
     // ---- loads: the tile and step that come next, and the rows of x that this wave's loads of it bring ----
@@ -499,6 +509,8 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_dw_kernel(const Pr
     int it = first, ik = 0, isteps = 0, lo = 0, rows = 0, index[4] = {0, 0, 0, 0};
     int64_t aoff[2], boff[2];                         // bytes within rows; -1: past the row's values
     auto look = [&]() __attribute__((always_inline)) {
+        if (ik == 0)
+            while (it < end && kept(it)) it += step;
         if (it >= end) return;
         if (ik == 0) {
             int e, a0, b0;
@@ -559,6 +571,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_dw_kernel(const Pr
         mark[i] = ops;
     }
     for (int t = first; t < end; t += step) {
+        if (kept(t)) continue;
         int e, a0, b0;
         find(t, e, a0, b0);
         const int steps = steps_of(rows_of(e));
