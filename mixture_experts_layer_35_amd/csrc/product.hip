@@ -473,6 +473,7 @@ constexpr int kDwStage = 2 * 32 * 512;
 constexpr int kDwSlots = 4;
 constexpr int kDwLds = kEndBytes + kDwSlots * kDwStage;
 
+template <bool ACCUMULATE>
 __global__ __launch_bounds__(kProductThreads, 1) void product_dw_kernel(const ProductPass a) {
     extern __shared__ __align__(1024) char smem[];
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -500,7 +501,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_dw_kernel(const Pr
     // an expert without rows takes one step of zeros, or none: added to, it keeps its values to the bit, so its tiles are passed
     // over by loads and products alike
     auto kept = [&](int t) {
-        return a.accumulate && rows_of(__builtin_amdgcn_readfirstlane(t / (atiles * btiles))) == 0;
+        return ACCUMULATE && rows_of(__builtin_amdgcn_readfirstlane(t / (atiles * btiles))) == 0;
     };
     auto steps_of = [&](int rows) { return max(1, parts_of(rows, 32)); };
 
@@ -540,7 +541,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_dw_kernel(const Pr
             const bool there = r < rows;
             const int64_t xrow = lane >> 5 ? index[q * 2 + 1] : index[q * 2];
             const char *x = (const char *)a.a + xrow * a.a_ld * 2 + aoff[q];
-            const char *y = (const char *)a.b + ((int64_t)lo + r) * a.b_ld * 2 + boff[q];
+            const char *y = (const char *)a.b + (int64_t)((uint32_t)lo + (uint32_t)r) * a.b_ld * 2 + boff[q];
             fill16(there && aoff[q] >= 0 ? x : (const char *)&product_zeros, stage + wid * 2048 + q * 1024);
             fill16(there && boff[q] >= 0 ? y : (const char *)&product_zeros, stage + kDwStage / 2 + wid * 2048 + q * 1024);
         }
@@ -611,7 +612,7 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_dw_kernel(const Pr
                     const int f = f0 + i * 16 + 4 * g;
                     const uint32_t at = f < a.A ? row + f * 4 : kNoOffset;
                     f32x4 v = acc[i][j];
-                    if (a.accumulate) v += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(out, at, 0, 0));
+                    if (ACCUMULATE) v += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(out, at, 0, 0));
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), out, at, 0, 0);
                 }
             } else {
@@ -863,7 +864,9 @@ hipError_t launch_product(int dt, int op, const ProductPass &p, hipStream_t s) {
                         (op == PRODUCT_DW ? p.A % 8 == 0 && p.B % 8 == 0
                                           : (int64_t)p.K * esz % 16 == 0 && (op == PRODUCT_Y || p.A % 8 == 0));
     if (op == PRODUCT_DW) {
-        if (pieces && p.wide) return product_launch<product_dw_kernel>(grid, kProductThreads, kDwLds, p, s);
+        if (pieces && p.wide)
+            return p.accumulate ? product_launch<product_dw_kernel<true>>(grid, kProductThreads, kDwLds, p, s)
+                                : product_launch<product_dw_kernel<false>>(grid, kProductThreads, kDwLds, p, s);
         return product_launch<product_kernel<DT_BF16, PRODUCT_DW, 4, false>>(grid, kProductThreads, kDwAnyLds, p, s);
     }
     auto of = [&](auto dtc, auto opc) {
