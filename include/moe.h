@@ -556,9 +556,12 @@ int moe_grouped_product_int8(int32_t n_exp, const int32_t *offsets, int64_t max_
  *   for each step k:  S = X X^T,  X <- a_k X + (b_k S + c_k S S) X;
  *   y = scale * X, turned back, bf16 [n][rows][cols] dense.
  * coeffs (host) holds a_k, b_k, c_k of the steps in turn, 3 * steps floats; 1 <= steps <= 64; eps >= 0.
- * The norm is held in 64 bits; X, S and their products in pairs of bf16, which keep 16 significant bits, with sums in fp32.
+ * The norm is held in 64 bits.  Operands of products are pairs of bf16, which keep 16 significant bits, with sums in fp32;
+ * the X of a_k X has all 24 bits of fp32 as long as the a of the steps left multiply by more than 64, so that rounding stays
+ * below a quarter of y's own in matrices of low rank too.
  * A matrix of zeros gives zeros (with eps > 0), one that holds an infinity or NaN gives NaN; other matrices do not
- * change.  Deterministic: sums depend on n, rows, cols and the card alone.  y may be g where g is bf16.
+ * change.  Deterministic: sums depend on n, rows, cols and the card alone.  y may be g where g is bf16 (the same address);
+ * otherwise they share no memory (a part of X lies in y between the steps).
  * With sides rounded up to multiples of 32: a matrix of at most 2^28 values, n of them below 2^40; the smaller side at
  * most 16384, n at most 65535.
  * ws: moe_orthogonalize_workspace_bytes(n, rows, cols).

@@ -1517,6 +1517,11 @@ int moe_orthogonalize(int64_t n, int32_t rows, int32_t cols, int32_t g_dtype, co
     ALIGNED(g, esize(g_dtype));
     ALIGNED(y, 2);
     TRY(ws_check(ws, ws_bytes, moe_orthogonalize_workspace_bytes(n, rows, cols), fn));
+    // y is written from the first kernel on
+    const int64_t values = n * rows * cols;
+    const uintptr_t g0 = (uintptr_t)g, y0 = (uintptr_t)y;
+    if (!(g0 == y0 && g_dtype == MOE_BF16) && g0 < y0 + values * 2 && y0 < g0 + values * esize(g_dtype))
+        return fail(MOE_ERR_INVALID_ARG, "%s: y overlaps g and is not g in bf16", fn);
     OrthProblem p{};
     p.n = n;
     p.rows = rows;

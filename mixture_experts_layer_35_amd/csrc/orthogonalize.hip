@@ -2,12 +2,22 @@
 //   X_0 = G / (|G|_F + eps);   S = X X^T,  P = b S + c S S,  X <- a X + P X
 // with G transposed where it has more rows than columns.
 //
-// X, S and P are held as pairs of bf16, hi = the nearest bf16 and lo = that of what is left: 2^-16 of a value at most is lost
-// (a step multiplies the smallest singular values, and errors beside them, by up to a = 3.4, so plain bf16 would
-// leave a few percent), and a product of pairs is three matrix products, hi hi + hi lo + lo hi, summed in fp32: lo lo is below
-// what the pair drops.  Rows of pairs hold 32 hi and then 32 lo of 32 values in turn, 128 bytes, which is what a step of the
-// reduction takes from a row.  Sides are padded to multiples of 32 with zeros.
+// Products take pairs of bf16, hi = the nearest bf16 and lo = that of what is left, which keep 16 significant bits: a product of
+// pairs is three matrix products, hi hi + hi lo + lo hi, summed in fp32 (lo lo is below what a pair drops).  Rows of pairs hold
+// 32 hi and then 32 lo of 32 values in turn, 128 bytes, which is what a step of the reduction takes from a row.  Sides are padded
+// to multiples of 32 with zeros.
+//
+// Plain bf16 would leave a few percent: a step multiplies the smallest singular values, and errors beside them, by up to
+// a = 3.4, five steps by 485.  What is multiplied so are errors outside both the rows' and the columns' space of X.  a X brings
+// such; P X lies in X's spaces on one side at least, whatever rounding P or X took, but for the dropped lo lo, ten times less.
+// So S and P are held in pairs, and the X that a multiplies in all of fp32's 24 bits, its last 8 (`rest`, a bf16 that is exact)
+// where y will be, as long as the steps left multiply by more than kRestGrowth: a pair loses 2^-18 of a value, which 64 times as
+// large is a seventh of what the result's rounding to bf16 loses.  Against 64 bits, before that rounding (1.7e-3), 512 x 1024:
+// rank 1 2.4e-4, rank 3 1.6e-4, full rank 3e-5; with X in pairs alone 1.7e-3, 1.1e-3 and 3e-5, with all bits in every step
+// 1.8e-4, 7.5e-5 and 3e-5, with everything in fp32 1.0e-4, 4.5e-5 and 2e-6.  8 matrices of 2048 x 7168 take 11.2 ms so and 11.0
+// with X in pairs alone, 24 of 1000 x 360 498 us and 478.
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "common.h"
@@ -21,12 +31,16 @@ namespace moe {
 namespace {
 
 constexpr int kOrthThreads = 512;
+constexpr double kRestGrowth = 64.0;
 
-// hi and lo of a value; a value that is not finite gives NaN in lo and so in every sum it meets.
+// hi and lo of a value (lo is rounded where it is stored); one that is not finite gives NaN in lo and so in every sum it meets.
 __device__ __forceinline__ void split_pair(float v, float &hi, float &lo) {
     hi = bf16_to_f32((uint16_t)pack_bf16x2(v, 0.0f));
     lo = v - hi;
 }
+
+// What hi and lo leave of a value: 8 bits, exact in bf16.
+__device__ __forceinline__ float rest_of(float lo) { return lo - bf16_to_f32((uint16_t)pack_bf16x2(lo, 0.0f)); }
 
 // ---- norms and the first X ---------------------------------------------------
 
@@ -80,11 +94,32 @@ __device__ __forceinline__ void store_pairs(uint16_t *row, int at, const float (
     *(u32x4 *)(to + 32) = ol;
 }
 
-// X_0 in pairs.  A workgroup takes 64 x 64 values; those of G^T (TALL) are turned over in LDS.
+// What pairs leave of eight values, `n` of which are there, to y (if any).
+__device__ __forceinline__ void store_rests(uint16_t *y, int64_t at, int n, const float (&v)[8]) {
+    if (!y) return;
+    float rest[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        float hi, lo;
+        split_pair(v[k], hi, lo);
+        rest[k] = rest_of(lo);
+    }
+    if (n >= 8) {
+        *(u32x4_any *)(y + at) = u32x4{pack_bf16x2(rest[0], rest[1]), pack_bf16x2(rest[2], rest[3]),
+                                       pack_bf16x2(rest[4], rest[5]), pack_bf16x2(rest[6], rest[7])};
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+        if (k < n) y[at + k] = (uint16_t)pack_bf16x2(rest[k], 0.0f);
+}
+
+// X_0 in pairs, and what they leave in y, which lies as G does and may be G: a thread writes there what it has read.
+// A workgroup takes 64 x 64 values; those of G^T (TALL) are turned over in LDS.
 template <int DT, bool TALL>
-__global__ __launch_bounds__(256) void orth_first_kernel(const void *__restrict__ g, const double *__restrict__ part,
-                                                         int parts, double eps, int r, int c, int rp, int cp,
-                                                         uint16_t *__restrict__ x) {
+__global__ __launch_bounds__(256) void orth_first_kernel(const void *g, const double *__restrict__ part, int parts,
+                                                         double eps, int r, int c, int rp, int cp,
+                                                         uint16_t *__restrict__ x, uint16_t *y) {
     const int m = blockIdx.z, c0 = blockIdx.x * 64, r0 = blockIdx.y * 64;
     const double inv = orth_inverse(part, m, parts, eps);
     const int64_t base = (int64_t)m * r * c;
@@ -98,7 +133,11 @@ __global__ __launch_bounds__(256) void orth_first_kernel(const void *__restrict_
             float v[8];
             load8<DT>(g, base + (int64_t)j * r + i, j < c ? r - i : 0, v);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) turned[(eight + q) * 65 + row + k] = v[q];
+            for (int q = 0; q < 8; ++q) {
+                v[q] = (float)((double)v[q] * inv);
+                turned[(eight + q) * 65 + row + k] = v[q];
+            }
+            store_rests(y, base + (int64_t)j * r + i, j < c ? r - i : 0, v);
         }
         __syncthreads();
     }
@@ -111,9 +150,10 @@ __global__ __launch_bounds__(256) void orth_first_kernel(const void *__restrict_
             for (int q = 0; q < 8; ++q) v[q] = turned[(row + k) * 65 + eight + q];
         } else {
             load8<DT>(g, base + (int64_t)i * c + j, i < r ? c - j : 0, v);
-        }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = (float)((double)v[q] * inv);
+            for (int q = 0; q < 8; ++q) v[q] = (float)((double)v[q] * inv);
+            store_rests(y, base + (int64_t)i * c + j, i < r ? c - j : 0, v);
+        }
         if (i < rp && j < cp) store_pairs(x + ((int64_t)m * rp + i) * cp * 2, j, v);
     }
 }
@@ -124,7 +164,8 @@ __global__ __launch_bounds__(256) void orth_first_kernel(const void *__restrict_
 //   GRAM    A, B: rows of X, k along them         S, symmetric
 //   SQUARE  A, B: rows of S                       P = c S S + b S, symmetric
 //   UPDATE  A: columns of X (k: its rows), B: rows of P      a X + P X
-enum { ORTH_GRAM, ORTH_SQUARE, ORTH_UPDATE };
+// SINGLE: the update of matrices whose y is taken value by value: X lies across it, or has fewer than four columns.
+enum { ORTH_GRAM, ORTH_SQUARE, ORTH_UPDATE, ORTH_UPDATE_SINGLE };
 
 struct OrthPass {
     int n;
@@ -132,8 +173,10 @@ struct OrthPass {
     const uint16_t *a, *b;      // pairs; rows of K (A: UPDATE rows of A)
     const uint16_t *c;          // what the epilogue adds, as out
     float alpha, beta;          // out = alpha * sum + beta * c
-    uint16_t *out;              // pairs, or
-    uint16_t *y;                // the result, bf16, [rows][cols] of G
+    uint16_t *out;              // pairs
+    uint16_t *y;                // UPDATE: [rows][cols] of G,
+    int rest_in, rest_out;      // what pairs leave of c and then of out,
+    int last;                   // or the result in bf16 (out is not written)
     int r, cc, tall;            // sides of X without padding
 };
 
@@ -150,7 +193,7 @@ struct OrthTile {
 template <int OP, int RB, int CAP, int WA>
 __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a) {
     typedef OrthTile<RB, CAP, WA> T;
-    constexpr bool SYM = OP != ORTH_UPDATE, ASTRIDED = OP == ORTH_UPDATE;
+    constexpr bool SINGLE = OP == ORTH_UPDATE_SINGLE, UPDATE = OP == ORTH_UPDATE || SINGLE, SYM = !UPDATE, ASTRIDED = UPDATE;
     constexpr int SLOTS = T::slots, STAGE = T::stage, WB = T::WB, QA = T::TA / 64, QB = T::TB / 64, N = QA + QB;
     constexpr int ROW = T::TA * 4, LANES = ROW / 16;   // a staged row of the reduction: bytes, lanes that bring it
     static_assert(T::TA % 64 == 0 && T::TB % 64 == 0 && RB % 2 == 0 && SLOTS >= 2, "loads of a step are shared evenly");
@@ -297,48 +340,111 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
         find(t, m, a0, b0);
         const bool mirror = SYM && b0 >= a0 + T::TA;
         const int64_t ld = (int64_t)a.A * 2, mat = (int64_t)m * a.B * ld;
+        // What is added to the sums of two blocks, the i-th and next of column j: loads without branches, two blocks ahead of the
+        // stores that they may not pass.  Rows
+        // and columns past the matrix repeat its last ones, and their sums are not stored; past X without padding rests are 0 (SINGLE
+        // loads read zeros past the matrix, and are masked like the others).
+        struct Added {
+            u32x2 hi[2], lo[2];
+            uint32_t rest[2][SINGLE ? 4 : 2];
+        } added[2];
+        // the matrix's X and y: bytes from their first value fit 32 bits
+        const char *const cm = (const char *)(a.c + mat);
+        char *const ym = (char *)(a.y + (int64_t)m * a.r * a.cc);
+        const uint32_t yb = a.tall ? 2 : 2 * (uint32_t)a.cc, yf = a.tall ? 2 * (uint32_t)a.r : 2;
+        __amdgpu_buffer_rsrc_t yr;
+        if constexpr (SINGLE) yr = buffer_of(ym, (int64_t)a.r * a.cc * 2);
+        auto load_added = [&](int j, int i0, Added &in) __attribute__((always_inline)) {
+            const int b = b0 + (j * WB + wm) * 16 + r15;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int f = a0 + wf * (RB * 16) + (i0 + i) * 16 + 4 * g;
+                const char *at = cm + ((uint32_t)min(b, a.B - 1) * a.A * 4 + min(f & ~31, a.A - 32) * 4 + (f & 31) * 2);
+                in.hi[i] = *(const u32x2 *)at;
+                in.lo[i] = *(const u32x2 *)(at + 64);
+                if (!UPDATE || !a.rest_in) continue;
+                if constexpr (UPDATE && SINGLE) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) in.rest[i][q] = __builtin_amdgcn_raw_buffer_load_b16(yr, b * yb + f * yf + q * yf, 0, 0);
+                } else if constexpr (UPDATE) {
+                    const u32x2 w = *(const u32x2_any *)(ym + (min(b, a.r - 1) * yb + min(f, a.cc - 4) * 2));
+                    in.rest[i][0] = w[0];
+                    in.rest[i][1] = w[1];
+                }
+            }
+        };
+        // four rests of X's row b from column f on, as they were loaded
+        auto rests = [&](const uint32_t *w, int b, int f, float (&v)[4]) __attribute__((always_inline)) {
+            uint64_t u;
+            if constexpr (SINGLE) {
+                u = (uint64_t)(w[2] | w[3] << 16) << 32 | (w[0] | w[1] << 16);
+            } else {
+                u = (uint64_t)w[1] << 32 | w[0];
+                const int past = f - min(f, a.cc - 4);
+                u = past >= 4 ? 0 : u >> (16 * past);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                v[q] = a.rest_in && b < a.r && f + q < a.cc ? bf16_to_f32((uint16_t)(u >> (16 * q))) : 0.0f;
+        };
+        // four values of y: each by the lane that has read it
+        auto y_store = [&](int b, int f, u32x2 w) __attribute__((always_inline)) {
+            if constexpr (SINGLE) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w[q >> 1] >> (16 * (q & 1))), yr,
+                                                          b < a.r && f + q < a.cc ? b * yb + f * yf + q * yf : kNoOffset, 0, 0);
+            } else if (b < a.r) {
+                if (f + 4 <= a.cc) {
+                    *(u32x2_any *)(ym + (b * yb + f * 2)) = w;
+                    return;
+                }
+#pragma unroll
+                for (int q = 0; q < 3; ++q)
+                    if (f + q < a.cc) *(uint16_t *)(ym + (b * yb + (f + q) * 2)) = (uint16_t)(w[q >> 1] >> (16 * (q & 1)));
+            }
+        };
+        if (OP != ORTH_GRAM) load_added(0, 0, added[0]);
 #pragma unroll
         for (int j = 0; j < CAP; ++j) {
             const int bb = b0 + (j * WB + wm) * 16, b = bb + r15;
 #pragma unroll
             for (int i = 0; i < RB; i += 2) {
                 const int f0 = a0 + wf * (RB * 16) + i * 16;           // a run of 32 values of a
+                const int u = (j * RB + i) / 2;
+                if (OP != ORTH_GRAM && u + 1 < CAP * RB / 2) load_added((i + 2) / RB + j, (i + 2) % RB, added[(u + 1) & 1]);
                 const bool there = b < a.B && f0 < a.A;
                 float v[2][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    u32x2 ch = {0, 0}, cl = {0, 0};
-                    if (OP != ORTH_GRAM && there) {
-                        const uint16_t *row = a.c + mat + b * ld + f0 * 2 + h * 16 + 4 * g;
-                        ch = *(const u32x2 *)row;
-                        cl = *(const u32x2 *)(row + 32);
-                    }
+                    const Added &in = added[u & 1];
+                    float rest[4] = {};
+                    if constexpr (UPDATE) rests(in.rest[h], b, f0 + h * 16 + 4 * g, rest);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float hi = bf16_to_f32((uint16_t)(ch[q >> 1] >> (16 * (q & 1))));
-                        const float lo = bf16_to_f32((uint16_t)(cl[q >> 1] >> (16 * (q & 1))));
                         v[h][q] = a.alpha * acc[i + h][j][q];
-                        if (OP != ORTH_GRAM) v[h][q] += a.beta * (hi + lo);
+                        if constexpr (OP != ORTH_GRAM) {
+                            const float hi = bf16_to_f32((uint16_t)(in.hi[h][q >> 1] >> (16 * (q & 1))));
+                            const float lo = bf16_to_f32((uint16_t)(in.lo[h][q >> 1] >> (16 * (q & 1))));
+                            v[h][q] += a.beta * (hi + lo + rest[q]);
+                        }
                     }
                 }
-                if (OP == ORTH_UPDATE && a.y) {
-                    const int64_t ym = (int64_t)m * a.r * a.cc;
+                if (UPDATE && a.last) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int f = f0 + h * 16 + 4 * g + q;
-                            if (b < a.r && f < a.cc)
-                                a.y[ym + (a.tall ? (int64_t)f * a.r + b : (int64_t)b * a.cc + f)] =
-                                    (uint16_t)pack_bf16x2(v[h][q], 0.0f);
-                        }
+                        y_store(b, f0 + h * 16 + 4 * g, u32x2{pack_bf16x2(v[h][0], v[h][1]), pack_bf16x2(v[h][2], v[h][3])});
                     continue;
                 }
                 float hi[2][4], lo[2][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) split_pair(v[h][q], hi[h][q], lo[h][q]);
+                    if (UPDATE && a.rest_out)
+                        y_store(b, f0 + h * 16 + 4 * g, u32x2{pack_bf16x2(rest_of(lo[h][0]), rest_of(lo[h][1])),
+                                                              pack_bf16x2(rest_of(lo[h][2]), rest_of(lo[h][3]))});
+                }
                 const u32x4 oh = pair_bf16_value(hi[0], hi[1], lane), ol = pair_bf16_value(lo[0], lo[1], lane);
                 if (there) {
                     uint16_t *row = a.out + mat + b * ld + f0 * 2 + pair_bf16_col(0, lane);
@@ -381,7 +487,7 @@ hipError_t orth_launch(unsigned grid, int lds, const OrthPass &p, hipStream_t s)
 template <int OP>
 hipError_t orth_product(const OrthPass &p, hipStream_t s) {
     const unsigned grid = (unsigned)((device_cus() + 7) / 8 * 8);
-    switch (orth_variant(p.n, p.A, p.B, OP != ORTH_UPDATE, grid)) {
+    switch (orth_variant(p.n, p.A, p.B, OP == ORTH_GRAM || OP == ORTH_SQUARE, grid)) {
         case kOrth256x256: return orth_launch<orth_kernel<OP, 4, 8, 4>>(grid, OrthTile<4, 8, 4>::lds, p, s);
         case kOrth256x128: return orth_launch<orth_kernel<OP, 4, 4, 4>>(grid, OrthTile<4, 4, 4>::lds, p, s);
         case kOrth128x128: return orth_launch<orth_kernel<OP, 2, 4, 4>>(grid, OrthTile<2, 4, 4>::lds, p, s);
@@ -418,11 +524,18 @@ hipError_t launch_orthogonalize(const OrthProblem &q, hipStream_t s) {
     poly = take(z.s);
     const int n = (int)q.n, r = (int)z.r, c = (int)z.c, rp = (int)z.rp, cp = (int)z.cp;
     const dim3 blocks((cp + 63) / 64, (rp + 63) / 64, n);
+    // the largest factor by which the steps from k on multiply what rounding adds to X_k
+    auto growth = [&](int k) {
+        double by = 1.0;
+        for (; k < q.steps; ++k) by *= fabs((double)q.coeffs[3 * k]);
+        return by;
+    };
+    uint16_t *const rests = growth(0) > kRestGrowth ? (uint16_t *)q.y : nullptr;
     auto first = [&](auto dtc) {
         constexpr int D = decltype(dtc)::value;
         orth_norm_kernel<D><<<n * z.parts, kNormThreads, 0, s>>>(q.g, z.r * z.c, z.parts, part);
-        if (z.tall) orth_first_kernel<D, true><<<blocks, 256, 0, s>>>(q.g, part, z.parts, q.eps, r, c, rp, cp, x[0]);
-        else orth_first_kernel<D, false><<<blocks, 256, 0, s>>>(q.g, part, z.parts, q.eps, r, c, rp, cp, x[0]);
+        if (z.tall) orth_first_kernel<D, true><<<blocks, 256, 0, s>>>(q.g, part, z.parts, q.eps, r, c, rp, cp, x[0], rests);
+        else orth_first_kernel<D, false><<<blocks, 256, 0, s>>>(q.g, part, z.parts, q.eps, r, c, rp, cp, x[0], rests);
     };
     if (q.dt == DT_F32) first(std::integral_constant<int, DT_F32>{});
     else first(std::integral_constant<int, DT_BF16>{});
@@ -453,11 +566,14 @@ hipError_t launch_orthogonalize(const OrthProblem &q, hipStream_t s) {
         p.alpha = scale;
         p.beta = co[0] * scale;
         p.out = x[(k + 1) & 1];
-        p.y = last ? (uint16_t *)q.y : nullptr;
+        p.y = (uint16_t *)q.y;
+        p.last = last;
+        p.rest_in = growth(k) > kRestGrowth;
+        p.rest_out = !last && growth(k + 1) > kRestGrowth;
         p.r = r;
         p.cc = c;
         p.tall = z.tall;
-        e = orth_product<ORTH_UPDATE>(p, s);
+        e = z.tall || z.c < 4 ? orth_product<ORTH_UPDATE_SINGLE>(p, s) : orth_product<ORTH_UPDATE>(p, s);
     }
     return e;
 }

@@ -74,6 +74,7 @@ __device__ __forceinline__ bf16x8 read_strided(const char *p) {
 // address.
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
 template <int DT>
 __device__ __forceinline__ void load8(const void *x, int64_t at, int64_t n, float (&v)[8]) {
     if (n >= 8) {

@@ -234,7 +234,8 @@ NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
 def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=None, eps: float = 1e-7, scale: float = 1.0,
                   out: torch.Tensor = None, stream=None) -> torch.Tensor:
     """scale times the matrices g [..., rows, cols] (bf16 or fp32, contiguous) brought near their nearest orthogonal ones by
-    Newton-Schulz steps, bf16.  coefficients: (a, b, c) for all steps or a list of them (default NEWTON_SCHULZ)."""
+    Newton-Schulz steps, bf16.  coefficients: (a, b, c) for all steps or a list of them (default NEWTON_SCHULZ).  out may be g in
+    bf16; otherwise they share no memory."""
     _on_gpu(g)
     _check("g", g, g.device, (torch.bfloat16, torch.float32), g.shape)
     rows, cols = g.shape[-2:]
