@@ -490,7 +490,8 @@ size_t moe_ffn_mx4_workspace_bytes(int64_t max_rows, int32_t inter);
  * the rows r in [offsets[e], offsets[e+1]) of a batch of max_rows rows.
  *   n_exp <= 1024 experts; offsets [n_exp+1] int32 on the device, offsets[0] = 0,
  *   non-decreasing, offsets[n_exp] <= max_rows < 2^31 (moe_permute gives them).  Rows from
- *   offsets[n_exp] on are neither read nor written; an expert may have none.
+ *   offsets[n_exp] on are neither read nor written; an expert may have none.  gather [max_rows] int32: each a row
+ *   of x, which is not checked.  Both 4-byte aligned.
  *   w [n_exp][out][in] dense; in and out any sizes up to 2^20 with in * out <= 2^29.
  *   Rows of the other matrices are *_ld elements apart (*_ld >= the row's values); addresses
  *   and rows at multiples of 16 bytes are the fast case, any other is taken.

@@ -1343,6 +1343,8 @@ int moe_grouped_product(int32_t n_exp, const int32_t *offsets, int64_t max_rows,
     NEED(x);
     NEED(w);
     NEED(y);
+    ALIGNED(offsets, 4);
+    ALIGNED(gather, 4);
     ALIGNED(x, 2);
     ALIGNED(w, 2);
     ALIGNED(y, esize(y_dtype));
@@ -1378,6 +1380,7 @@ int moe_grouped_product_dx(int32_t n_exp, const int32_t *offsets, int64_t max_ro
     NEED(dy);
     NEED(w);
     NEED(dx);
+    ALIGNED(offsets, 4);
     ALIGNED(dy, 2);
     ALIGNED(w, 2);
     ALIGNED(dx, esize(dx_dtype));
@@ -1415,6 +1418,8 @@ int moe_grouped_product_dw(int32_t n_exp, const int32_t *offsets, int64_t max_ro
         NEED(x);
         NEED(dy);
     }
+    ALIGNED(offsets, 4);
+    ALIGNED(gather, 4);
     ALIGNED(x, 2);
     ALIGNED(dy, 2);
     ALIGNED(dw, esize(dw_dtype));
@@ -1471,6 +1476,8 @@ int moe_grouped_product_int8(int32_t n_exp, const int32_t *offsets, int64_t max_
     NEED(w);
     NEED(w_scales);
     NEED(y);
+    ALIGNED(offsets, 4);
+    ALIGNED(gather, 4);
     ALIGNED(x, 16);
     ALIGNED(w, 16);
     ALIGNED(x_scales, 4);
