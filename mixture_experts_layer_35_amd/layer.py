@@ -55,6 +55,8 @@ def _torch_stream(stream, device) -> torch.cuda.Stream:
         return torch.cuda.current_stream(device)
     if isinstance(stream, int):
         return torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    if stream.device != torch.device(device):
+        raise ValueError("a stream of %s expected, not of %s" % (device, stream.device))
     return stream
 
 
