@@ -499,6 +499,7 @@ size_t moe_ffn_mx4_workspace_bytes(int64_t max_rows, int32_t inter);
  * output's type, MOE_BF16 or MOE_F32.  Deterministic: the order of a sum depends on the sizes, the
  * alignment and the card alone, so a row among more rows can differ in a sum's last bit.
  * Infinities and NaN go where the formula takes them, and to no other row or feature.
+ * Results share no memory with the other arguments.
  */
 
 /*

@@ -138,13 +138,34 @@ def _batch(offsets, gather, n, rows, device):
     return gather.numel()
 
 
-def _out(name, out, shape, dtype, device):
+def _out(name, out, shape, dtype, device, *inputs):
     if dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("%s: bf16 or fp32 expected, not %s" % (name, dtype))
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _check(name, out, device, (dtype,), shape, dense=False)
+    _apart(name, out, *inputs)
     return out
+
+
+def _place(t):
+    """First byte, bytes of a row, bytes from row to row and the byte behind the last of a matrix of rows or a dense tensor."""
+    size = t.element_size()
+    rows, cols, ld = (1, t.numel(), t.numel()) if t.is_contiguous() else (*t.shape, _row_stride(t))
+    return t.data_ptr(), cols * size, ld * size, t.data_ptr() + ((rows - 1) * ld + cols) * size
+
+
+def _apart(name, out, *inputs):
+    """Refuses a result over an input: kernels write it while they still read.  Columns of one buffer beside each other are apart."""
+    first, width, step, end = _place(out)
+    for t in inputs:
+        at, w, ld, behind = _place(t)
+        if not out.numel() or not t.numel() or first >= behind or at >= end:
+            continue
+        # rows of the same spacing: apart where the one's columns lie in the gap behind the other's
+        if step == ld and w <= (first - at) % ld <= ld - width:
+            continue
+        raise ValueError("%s shares memory with an input" % name)
 
 
 def grouped_product(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, gather: torch.Tensor = None,
@@ -152,14 +173,15 @@ def grouped_product(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, gat
     """y[r] = w[e] x[gather[r]] for the rows offsets[e] <= r < offsets[e + 1] of expert e.
 
     x [tokens][in] bf16 (rows may be padded), w [n][out][in] bf16, offsets [n + 1] and gather [rows] int32 (None: a row for
-    each token), all on one GPU; y [rows][out] bf16 or fp32.  Rows from offsets[n] on are left as they were."""
+    each token), all on one GPU; y [rows][out] bf16 or fp32.  Rows from offsets[n] on are left as they were; out shares no memory
+    with the inputs."""
     _on_gpu(x, w, offsets)
     n, cout, cin = w.shape
     _check("x", x, w.device, (torch.bfloat16,), (x.shape[0], cin), dense=False)
     _check("w", w, w.device, (torch.bfloat16,), w.shape)
     rows = _batch(offsets, gather, n, x.shape[0], w.device)
     with _at(stream, w.device):
-        y = _out("out", out, (rows, cout), dtype, w.device)
+        y = _out("out", out, (rows, cout), dtype, w.device, x, w)
         moe_grouped_product(n, offsets, rows, gather, cin, cout, x, _row_stride(x), w, _float_type(y), y, _row_stride(y))
     return y
 
@@ -174,7 +196,7 @@ def grouped_product_dx(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     _check("w", w, w.device, (torch.bfloat16,), w.shape)
     rows = _batch(offsets, None, n, dy.shape[0], w.device)
     with _at(stream, w.device):
-        dx = _out("out", out, (rows, cin), dtype, w.device)
+        dx = _out("out", out, (rows, cin), dtype, w.device, dy, w)
         moe_grouped_product_dx(n, offsets, rows, cin, cout, dy, _row_stride(dy), w, _float_type(dx), dx, _row_stride(dx))
     return dx
 
@@ -191,7 +213,7 @@ def grouped_product_dw(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tensor,
     with _at(stream, x.device):
         if add_to is not None:
             _check("add_to", add_to, x.device, (torch.float32,), (n, cout, cin))
-        dw = _out("dw", add_to, (n, cout, cin), torch.float32 if add_to is not None else dtype, x.device)
+        dw = _out("dw", add_to, (n, cout, cin), torch.float32 if add_to is not None else dtype, x.device, x, dy)
         moe_grouped_product_dw(n, offsets, rows, gather, cin, cout, x, _row_stride(x), dy, _row_stride(dy), _float_type(dw),
                                dw, add_to is not None)
     return dw
@@ -224,7 +246,7 @@ def grouped_product_int8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tenso
     _check("w_scales", w_scales, w.device, (torch.float32,), (n, cout))
     rows = _batch(offsets, gather, n, x.shape[0], w.device)
     with _at(stream, w.device):
-        y = _out("out", out, (rows, cout), dtype, w.device)
+        y = _out("out", out, (rows, cout), dtype, w.device, x, x_scales, w, w_scales)
         moe_grouped_product_int8(n, offsets, rows, gather, cols, cout, x, x_scales, w, w_scales, _float_type(y), y,
                                  _row_stride(y))
     return y
