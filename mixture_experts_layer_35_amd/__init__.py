@@ -38,7 +38,8 @@ EXPORTED = ("moe_route", "moe_permute", "moe_grouped_ffn", "moe_combine", "moe_f
             "moe_quantize_1x128", "moe_quantize_weights_128x128", "moe_quantize_128x1", "moe_gate",
             "moe_gate_backward", "moe_quantize_mx4", "moe_dequantize_mx4", "moe_grouped_ffn_mx4",
             "moe_ffn_mx4_workspace_bytes", "moe_grouped_product", "moe_grouped_product_dx", "moe_grouped_product_dw",
-            "moe_quantize_int8", "moe_grouped_product_int8", "moe_orthogonalize", "moe_orthogonalize_workspace_bytes", "moe_last_error", "moe_version")
+            "moe_quantize_int8", "moe_grouped_product_int8", "moe_orthogonalize", "moe_orthogonalize_workspace_bytes",
+            "moe_last_error", "moe_version")
 
 
 class MoeError(RuntimeError):

@@ -325,7 +325,8 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
             }
 #pragma unroll
             for (int j = 0; j < CAP; ++j) {
-                const bf16x8 bh = *(const bf16x8 *)(bs + blo + j * (WB * 2048)), bl = *(const bf16x8 *)(bs + (blo ^ 64) + j * (WB * 2048));
+                const bf16x8 bh = *(const bf16x8 *)(bs + blo + j * (WB * 2048));
+                const bf16x8 bl = *(const bf16x8 *)(bs + (blo ^ 64) + j * (WB * 2048));
 #pragma unroll
                 for (int i = 0; i < RB; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ah[i], bh, acc[i][j], 0, 0, 0);
 #pragma unroll
@@ -341,9 +342,8 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
         const bool mirror = SYM && b0 >= a0 + T::TA;
         const int64_t ld = (int64_t)a.A * 2, mat = (int64_t)m * a.B * ld;
         // What is added to the sums of two blocks, the i-th and next of column j: loads without branches, two blocks ahead of the
-        // stores that they may not pass.  Rows
-        // and columns past the matrix repeat its last ones, and their sums are not stored; past X without padding rests are 0 (SINGLE
-        // loads read zeros past the matrix, and are masked like the others).
+        // stores that they may not pass.  Rows and columns past the matrix repeat its last ones, and their sums are not stored;
+        // past X without padding rests are 0 (SINGLE loads read zeros past the matrix, and are masked like the others).
         struct Added {
             u32x2 hi[2], lo[2];
             uint32_t rest[2][SINGLE ? 4 : 2];
@@ -365,7 +365,8 @@ __global__ __launch_bounds__(kOrthThreads, 1) void orth_kernel(const OrthPass a)
                 if (!UPDATE || !a.rest_in) continue;
                 if constexpr (UPDATE && SINGLE) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) in.rest[i][q] = __builtin_amdgcn_raw_buffer_load_b16(yr, b * yb + f * yf + q * yf, 0, 0);
+                    for (int q = 0; q < 4; ++q)
+                        in.rest[i][q] = __builtin_amdgcn_raw_buffer_load_b16(yr, b * yb + f * yf + q * yf, 0, 0);
                 } else if constexpr (UPDATE) {
                     const u32x2 w = *(const u32x2_any *)(ym + (min(b, a.r - 1) * yb + min(f, a.cc - 4) * 2));
                     in.rest[i][0] = w[0];

@@ -283,8 +283,9 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
         }
         return n;
     };
-    // the same through registers, for rows that do not lie at multiples of 16 bytes: two sets, so that a step's loads have two steps'
-    // time (4 rows to 4 experts of 6581 x 1793, the gradient at x: 79 us, with one set 141)
+    // the same through registers, for rows that do not lie at multiples of 16 bytes: two sets, so that a step's loads have two
+    // steps' time (4 rows to 4 experts of 6581 x 1793, the gradient at x: 79 us, with one set 141).  The second set does not quite
+    // fit: the product spills 14 registers and the gradient at x 21, 60 and 88 bytes of scratch a lane
     u32x4 areg[2][4], breg[2][DW ? 4 : QB];
     int iblocks[2] = {0, 0};
     auto fetch = [&](auto setc) __attribute__((always_inline)) {
@@ -318,7 +319,8 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
                     const int row = arow0 + q * 8;
                     areg[S][q] = none;
                     if (ia0 + wid * 32 + q * 8 < a.A) {          // the load's first row, the same in all lanes
-                        const u32x4 v = row_chunk(m + (int64_t)min(ia0 + row, a.A - 1) * a.a_ld, ik * 64 + bytes_at(row) / 2, a.K);
+                        const uint16_t *from = m + (int64_t)min(ia0 + row, a.A - 1) * a.a_ld;
+                        const u32x4 v = row_chunk(from, ik * 64 + bytes_at(row) / 2, a.K);
                         areg[S][q] = ia0 + row < a.A ? v : none;
                     }
                 } else {
@@ -463,12 +465,13 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_kernel(const Produ
     }
 }
 
-// dw for operands and results at multiples of 16 bytes.  A tile is 256 inputs by 256 features of one expert; the expert's rows are
-// taken 32 at a time through a ring of four stages, of which three are under way (with two stages of 64 rows, whose gather
-// indexes were vector loads that every load under way had to end for, 32 experts of 512 rows took 1165 us).  The rows' indexes come
-// by scalar loads a stage ahead.  Results leave by stores without branches, so that their number is known: a stage's loads
+// dw for operands and results at multiples of 16 bytes.  A tile is 256 inputs by 256 features of one expert; the expert's rows
+// are taken 32 at a time through a ring of four stages, of which three are under way (with two stages of 64 rows, whose gather
+// indexes were vector loads that every load under way had to end for, 32 experts of 512 rows took 1165 us).  The rows' indexes
+// come by scalar loads a stage ahead.  Results leave by stores without branches, so that their number is known: a stage's loads
 // are waited for by counting what was issued behind them, and the stores of one tile drain under the next.  Tiles are listed in
-// groups of 8 along a, so that the 32 of an XCD share 8 blocks of x and 4 of dy.
+// groups of 8 along a, so that the 32 of an XCD share 8 blocks of x and 4 of dy.  32 experts of 512 rows, 7168 by 2048: 845 us
+// in fp32 (1.9 GB of results; 0.57 PFLOP/s), 664 in bf16, 1270 in fp32 added to what is there.
 constexpr int kDwStage = 2 * 32 * 512;
 constexpr int kDwSlots = 4;
 constexpr int kDwLds = kEndBytes + kDwSlots * kDwStage;
@@ -633,7 +636,8 @@ __global__ __launch_bounds__(kProductThreads, 1) void product_dw_kernel(const Pr
 // Few tiles: a single token to its experts, small matrices.  Bound by the time from one load to the next, so the work is cut
 // finely: a tile is 64 values of a by up to 8 rows of b, and the four waves of a workgroup share it, each a quarter of the steps,
 // which pass through a ring in LDS of the wave's own without barriers.  The sums meet in LDS, in the order of the waves.
-// One token, 8 experts of 7168 x 2048 (235 MB): 50 us against 69 in tiles of 256.
+// One token, 8 experts of 7168 x 2048 (235 MB): 43 us with other experts in each call (36 with the same ones, whose weights the
+// last cache then holds in part), 69 in tiles of 256 by 160 rows.
 constexpr int kStreamThreads = 256;
 constexpr int kStreamRows = product_rows(kProductStream);
 constexpr int kStreamStageA = 64 * 128, kStreamStage = kStreamStageA + kStreamRows * 128, kStreamSlots = 4;
@@ -789,8 +793,10 @@ hipError_t product_launch(unsigned grid, int threads, int lds, const ProductPass
 
 // ---- rounding to 8-bit integers ----------------------------------------------
 
-// A row's largest magnitude, then its codes.  WAVES waves take a row, eight values a lane at a time; up to four times eight stay in registers between the two, longer rows are read again.  A row of 7168 by one wave
-// takes 47 us however few there are, by four 4.6; short rows keep more lanes at work with a wave each.
+// A row's largest magnitude, then its codes.  WAVES waves take a row, eight values a lane at a time; up to four times eight stay
+// in registers between the two, longer rows are read again.  By one wave and by four: 4096 rows of 512 4.5 and 8.8 us, of 2048
+// 5.3 and 9.7, of 4096 9.8 and 12.2, of 7168 20.2 and 17.3; 64 rows of 4096 5.2 and 4.6, of 7168 8.0 and 4.6 (4.5 is the host's
+// call).  One wave takes what it can hold: up to 2048 values.
 constexpr int kInt8Held = 4;
 
 template <int DT, int WAVES>

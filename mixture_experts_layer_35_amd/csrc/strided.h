@@ -30,8 +30,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, int64
 // for, and the compiler does not know that they write LDS: with the builtins it waits for every load under way before each
 // transpose read of LDS (512 rows an expert, the gradient at x: 1080 us of loads and reads against 385 without the reads).
 // Nor does it count them when it waits for loads of its own, which then takes longer than it has to: values that such loads bring
-// are settled (arrived) before the next direct load.  Whoever reads what they bring waits for them by itself (wait_vmcnt and a barrier).  M0 holds the place; kernels with these loads use
-// nothing else that reads M0.
+// are settled (arrived) before the next direct load.  Whoever reads what they bring waits for them by itself (wait_vmcnt and a
+// barrier).  M0 holds the place; kernels with these loads use nothing else that reads M0.
 __device__ __forceinline__ int lds_place(const void *p) {
     return (int)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
 }
@@ -70,8 +70,8 @@ __device__ __forceinline__ bf16x8 read_strided(const char *p) {
     return __builtin_bit_cast(bf16x8, (v8s)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Eight values of a fp32 or bf16 array from `at` on, zeros past n of them: 16-byte accesses, which the memory pipeline takes at every
-// address.
+// Eight values of a fp32 or bf16 array from `at` on, zeros past n of them: 16-byte accesses, which the memory pipeline takes at
+// every address.
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(2)));

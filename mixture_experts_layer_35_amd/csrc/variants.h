@@ -63,24 +63,36 @@ inline Mx4Variant mx4_variant(int64_t max_rows, int64_t n_exp, int64_t kruns, in
 
 // ---- products of experts -------------------------------------------------------
 enum ProductVariant {
-    kProductAny,        // operands through registers: rows that do not lie at multiples of 16 bytes
+    kProductAny,        // operands through registers: where one of them does not lie in pieces of 16 bytes
     kProductStream,     // tiles of 64 features by up to 8 rows, four waves a tile
     kProduct160,        // tiles of 256 features by up to 160 rows, three stages of LDS
     kProduct256,        // by up to 256 rows, two stages
 };
 
 // Rows of a tile.
-constexpr int product_rows(ProductVariant v) { return v == kProductStream ? 8 : v == kProduct160 ? 160 : v == kProduct256 ? 256 : 128; }
+constexpr int product_rows(ProductVariant v) {
+    return v == kProductStream ? 8 : v == kProduct160 ? 160 : v == kProduct256 ? 256 : 128;
+}
 
-// features: the output's (the inputs of the gradient at x); pieces: whether operands lie in pieces of 16 bytes.
+// features: the output's (the inputs of the gradient at x); pieces: whether both operands lie in pieces of 16 bytes.  Where one
+// does not, both go through registers, and few rows lose most: one token to 8 experts of 7161 x 2048 246 us, of 7168 x 2048 43;
+// 2 tokens to 16 experts of 7168 x 2048 333 us with x's rows 3 values wider, 79 without; 128 tokens, 256 experts 2730 and 1190.
 inline ProductVariant product_variant(int64_t max_rows, int64_t n_exp, int64_t features, bool pieces, int64_t cus) {
     if (!pieces) return kProductAny;
     const int64_t experts = max_rows < n_exp ? max_rows : n_exp;
-    // small tiles as long as there are no more than two for each compute unit
+    // Small tiles as long as there are no more than two for each compute unit.  Small tiles and tiles of 160 rows, experts of one
+    // row each, in microseconds: 7168 to 2048, 8 experts (256 small tiles) 35 and 69, 16 (512) 79 and 96, 24 (768) 117 and 118;
+    // 512 to 512, 64 experts (512) 7.5 and 9.1, 96 (768) 11.1 and 10.5; the gradient at x of 2048 to 7168, 12 experts (384) 76
+    // and 85, 16 (512) 90 and 89, 24 (768) 133 and 115; 8 bits, 7168 to 2048, 12 experts 34 and 39, 16 40 and 39, 24 66 and 61.
     const int64_t small = (experts + (max_rows - experts) / product_rows(kProductStream)) * ((features + 63) / 64);
     if (small <= 2 * cus) return kProductStream;
-    // 32 experts, 512 rows: 7168 to 2048 577 us in tiles of 256 rows.  256 experts, 128 rows: 1560 us in tiles of 160 with a stage
-    // more, 1686 with 128, which half of the experts need two of
+    // Tiles of 160 rows, which leave room for a stage more, where experts of the average size need one of them.  7168 to 2048, 32
+    // experts of as many rows each, tiles of 160 and of 256: 128 rows 181 and 205 us, 160 rows 200 and 215, 170 rows 277 and 220,
+    // 256 rows 287 and 259, 320 rows 342 and 347, 512 rows 522 and 466.  The host does not know how rows are spread: 150 on
+    // average and 183 at most takes tiles of 160, 313 us against 214; 200 on average and 1539 at most tiles of 256, 394 against
+    // 295.  Nor does the rule look at how many tiles there are: 8 experts of 256 rows, 2048 to 2048, take 54 us in 64 tiles of
+    // 256 and would take 37 in 128 of 160.  256 experts of 128 rows: 1560 us with 160, 1686 with 128, which half of the experts
+    // need two of.
     return max_rows > 160 * n_exp ? kProduct256 : kProduct160;
 }
 
@@ -90,7 +102,11 @@ enum OrthVariant { kOrth256x256, kOrth256x128, kOrth128x128, kOrth64x64 };   // 
 // The tiles that end soonest: rounds of tiles over the workgroups, each as long as one tile takes.  A tile of 256 x 256 takes
 // 2.2 to 3.1 times as long as one of 128 x 128, one of 256 x 128 1.4 to 1.7 times.  Microseconds with 256 x 256, 256 x 128 and
 // 128 x 128: 8 matrices of 2048 x 7168, X X^T 907, 818, 887, P X 1178, 1349, 1621; one of them 381, 236, 169 and 150, 178,
-// 225; 32 of 512 x 1024, X X^T 70, 45, 57.
+// 225; 32 of 512 x 1024, X X^T 70, 45, 57.  Whole calls of five steps with one product's tile changed, 256 x 256, 256 x 128,
+// 128 x 128 and 64 x 64, X X^T and S S / P X: one matrix of 256 x 512 387, 258, 201, 138 / 277, 207, 168, 137; 8 of 300 x 700
+// 502, 346, 279, 201 / 321, 244, 203, 201; 8 of 512 x 1024 724, 493, 381, 389 / 544, 443, 389, 470; 100 of 200 x 200 397, 309,
+// 350, 339 / 368, 308, 324, 381; 24 of 360 x 1000 791, 612, 504, 506 / 506, 535, 517, 605.  The rule took the least or one
+// within 3 % of it at 15 sizes.
 inline OrthVariant orth_variant(int64_t n, int64_t A, int64_t B, bool symmetric, int64_t workgroups) {
     auto time = [&](int64_t ta, int64_t tb, int64_t tile) {
         const int64_t at = (A + ta - 1) / ta, bt = (B + tb - 1) / tb;

@@ -120,6 +120,7 @@ def dequantize_mx4(q: torch.Tensor, s: torch.Tensor, cols: int, dtype=torch.bflo
 
 
 # ---- products of experts ------------------------------------------------------------------------
+# Autograd does not record these calls, also where an input requires a gradient: gradients are calls of their own.
 
 
 @contextlib.contextmanager
@@ -156,7 +157,8 @@ def _place(t):
 
 
 def _apart(name, out, *inputs):
-    """Refuses a result over an input: kernels write it while they still read.  Columns of one buffer beside each other are apart."""
+    """Refuses a result over an input: kernels write it while they still read.  Columns of one buffer beside each other are
+    apart."""
     first, width, step, end = _place(out)
     for t in inputs:
         at, w, ld, behind = _place(t)
@@ -174,7 +176,7 @@ def grouped_product(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, gat
 
     x [tokens][in] bf16 (rows may be padded), w [n][out][in] bf16, offsets [n + 1] and gather [rows] int32 (None: a row for
     each token), all on one GPU; y [rows][out] bf16 or fp32.  Rows from offsets[n] on are left as they were; out shares no memory
-    with the inputs."""
+    with the inputs.  Autograd does not record it: grouped_product_dx and grouped_product_dw are its gradients."""
     _on_gpu(x, w, offsets)
     n, cout, cin = w.shape
     _check("x", x, w.device, (torch.bfloat16,), (x.shape[0], cin), dense=False)
@@ -236,7 +238,7 @@ def grouped_product_int8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tenso
                          offsets: torch.Tensor, gather: torch.Tensor = None, dtype=torch.bfloat16,
                          out: torch.Tensor = None, stream=None) -> torch.Tensor:
     """grouped_product of quantize_int8's tokens x [tokens][128 R], x_scales [tokens] and weights w [n][out][128 R], w_scales
-    [n][out], of `cols` values a row."""
+    [n][out], of `cols` values a row.  It has no gradient."""
     _on_gpu(x, x_scales, w, w_scales, offsets)
     n, cout = w_scales.shape
     run = -(-cols // 128) * 128
