@@ -56,3 +56,21 @@ def test_few_values(moe, rows, cols):
     for i in range(n):
         check(y[i], *bounds(g[i]))
     assert out[0] == 7 and (out[1 + n * rows * cols:] == 7).all()
+
+
+@pytest.mark.parametrize("rows,cols", [(300, 130), (130, 300)], ids=["tall", "wide"])
+@pytest.mark.parametrize("coeffs", [MUON * 4 + (100.0, -120.0, 21.0), (100.0, -120.0, 21.0) + (0.1, 0.2, 0.1), MUON, (65.0, 0.0, 0.0)],
+                         ids=["last", "first", "one", "only"])
+def test_steps_that_grow_differently(moe, rows, cols, coeffs):
+    """The last step takes all bits of X too where it multiplies by much, or a step in the middle does not: in place and elsewhere
+    the same bits, and the formula's values."""
+    from test_gpu_orthogonalize import check, exact as bounds
+    g = matrices(20, rows, cols, 0).to(torch.bfloat16)
+    gd = g.cuda()
+    ws = torch.empty(moe.moe_orthogonalize_workspace_bytes(20, rows, cols), dtype=torch.uint8, device="cuda")
+    y = torch.full_like(gd, float("nan"))
+    for out in (y, gd):
+        moe.moe_orthogonalize(20, rows, cols, moe.MOE_BF16, gd, len(coeffs) // 3, coeffs, 1e-7, 1.0, out, ws)
+    assert torch.equal(y, gd)
+    for i in (0, 19):
+        check(y[i], *bounds(g[i], coeffs))
