@@ -9,6 +9,7 @@ the device by ``moe_quantize_weights_128x128`` (128 x 128 blocks, §3.3 of the
 from __future__ import annotations
 
 import contextlib
+import math
 
 import numpy as np
 import torch
@@ -164,8 +165,9 @@ def _apart(name, out, *inputs):
         at, w, ld, behind = _place(t)
         if not out.numel() or not t.numel() or first >= behind or at >= end:
             continue
-        # rows of the same spacing: apart where the one's columns lie in the gap behind the other's
-        if step == ld and w <= (first - at) % ld <= ld - width:
+        # rows at multiples of `every`: apart where the one's columns lie in the gap behind the other's
+        every = math.gcd(step, ld)
+        if w <= (first - at) % every <= every - width:
             continue
         raise ValueError("%s shares memory with an input" % name)
 
